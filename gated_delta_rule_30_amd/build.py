@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_scan.hip", "kda_bwd.hip",
-           "kda_wide.hip", "kda_noalloc.hip", "kda_prologue.hip"]
+           "kda_wide.hip", "kda_noalloc.hip", "kda_prologue.hip", "kda_paged_api.cpp",
+           "kda_rope.hip", "kda_attn.hip", "kda_pages.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
