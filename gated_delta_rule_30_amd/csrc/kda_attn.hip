@@ -1,68 +1,463 @@
-// Causal attention of new tokens over a paged KV cache (include/kda_paged.h).
-#include "kda_device.h"
-#include "kda_paged_int.h"
+// Causal attention of few new tokens over a paged KV cache: the decode step, speculative and
+// short chunks (kda_attn_tile.hip takes the long ones).
+//
+//   o_t = sum_j softmax_j(scale q_t . k_j) v_j,  one pass over the keys with a running maximum m
+//   and sum l: o <- o e^{m - m'} + sum_j e^{s_j - m'} v_j,  l likewise, o / l at the end.
+//
+// Bound by HBM: every key and value is read once for the G query heads (times new tokens) that
+// share it, 4 G flops per byte of bf16. So the work is laid out for bytes in flight:
+//  - The keys of all (sequence, K/V head, 16-row tile) items are laid end to end in units of 128
+//    (fp32: 64) keys and cut into equal shares, one per workgroup, wherever the borders fall: a
+//    ragged batch loads every compute unit alike. An item that is cut leaves partial (o, m, l) in the
+//    workspace, which a second launch joins.
+//  - A unit is four blocks of 32 (fp32: 16) keys, one per wave; the waves run on their own, with
+//    the next block's keys and values in flight in registers while one is computed, and meet at
+//    the item's end.
+// Scores are formed transposed, S^T = K Q^T, so that a lane holds scores of one row: the maximum
+// and sum are register loops and two lane exchanges, and the weights are already laid out as the
+// second operand of O^T = V^T P^T. K goes from memory straight to the operand registers; V
+// passes through LDS, where it is read transposed.
+#include "kda_attn.h"
 
 namespace kda {
 
 namespace {
 
-__device__ __forceinline__ int64_t first_row(const PagedBatch& b, int n) {
-  if (!b.cu_seqlens) return b.total_tokens / b.num_seqs * n;
-  const int64_t c = b.cu_seqlens[n];
-  return c < 0 ? 0 : c > b.total_tokens ? b.total_tokens : c;
+constexpr int kThreads = 256, kWaves = 4;
+constexpr int kGroups = 512;  // workgroups of the row kernel: two per compute unit
+
+template <typename MT, int D>
+struct Row {
+  typedef typename Mma<MT>::frag frag;
+  static constexpr int ES = sizeof(MT), KS = Mma<MT>::KS, EPL = Mma<MT>::EPL;
+  static constexpr int UNIT = kWaves * KS;      // keys of a unit
+  static constexpr int NG = KS / 16;            // 16-key groups of a block
+  static constexpr int SK = D / KS;             // reduction steps of a score
+  static constexpr int NC = D / 16;             // 16-channel tiles of the output
+  static constexpr int RC = D * ES / 16;        // 16-byte parts of a row
+  static constexpr int RPI = 64 / RC;           // rows that one wave-wide load covers
+  static constexpr int VL = KS / RPI;           // such loads of a block
+  static constexpr int TILE = KS * D * ES;      // bytes of a block's values in LDS
+  static constexpr int OBYTES = 16 * D * 4;     // bytes of one wave's output tile
+  static constexpr int LDS = kWaves * (TILE > OBYTES ? TILE : OBYTES);
+};
+
+// Byte offset of 16-byte part `part` of row `row` of a block's values in LDS. Parts are permuted
+// within a row so that the transposed reads of a 16-lane group (bf16: 4 rows x 2 parts; fp32: one
+// channel run in 4 rows of 4) touch every bank once.
+template <typename MT, int D>
+__device__ __forceinline__ int v_at(int row, int part) {
+  const int sw = sizeof(MT) == 2 ? (row & 3) << 1 : ((row >> 2) & 3) << 2;
+  return row * (D * (int)sizeof(MT)) + (part ^ sw) * 16;
 }
 
-// One wave per (token, query head): D / 64 channels per lane, one key at a time.
-template <typename T, int D>
-__global__ __launch_bounds__(64) void attn_kernel(AttnArgs a) {
-  constexpr int E = D / 64;
-  const int64_t t = blockIdx.x / a.num_q_heads;
-  const int hq = (int)(blockIdx.x - t * a.num_q_heads), h = hq / (a.num_q_heads / a.num_kv_heads);
-  int n = 0;
-  while (n < a.b.num_seqs && first_row(a.b, n + 1) <= t) ++n;
-  if (n == a.b.num_seqs || t < first_row(a.b, 0)) return;
-  const int ps = a.b.page_size;
-  const int64_t p = a.b.seq_lens[n] - (first_row(a.b, n + 1) - t);
-  const int64_t lo = a.window ? max((int64_t)0, p - a.window + 1) : 0;
-  const int64_t hi = min(p, (int64_t)a.b.max_pages * ps - 1);
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e)
-    q[e] = to_f32<T>(((const T*)a.q)[t * a.q_stride + hq * D + e * 64 + threadIdx.x]) * a.scale;
-  for (int64_t j = lo; j <= hi; ++j) {
-    const int pg = a.b.block_table[n * a.b.table_stride + j / ps];
-    if ((unsigned)pg >= (unsigned)a.b.num_pages) continue;
-    const int64_t at = ((int64_t)h * ps + j % ps) * D + threadIdx.x;
-    const T* k = (const T*)a.k_pages + pg * a.k_page_stride + at;
-    const T* v = (const T*)a.v_pages + pg * a.v_page_stride + at;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += q[e] * to_f32<T>(k[e * 64]);
-    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    if (s == -INFINITY) continue;
-    const float mn = fmaxf(m, s), al = expf(m - mn), w = expf(s - mn);
-    l = l * al + w;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * al + w * to_f32<T>(v[e * 64]);
-    m = mn;
+// Fragment of V^T: channels 16 c .. + 15, the block's keys.
+template <int D>
+__device__ __forceinline__ bf16x8 v_frag(const char* v, int c, int m, int g, bf16) {
+  const int part = 2 * c + ((m & 3) >> 1), row = 4 * g + (m >> 2);
+  const bf16x4 lo = ds_read_tr4((const bf16*)(v + v_at<bf16, D>(row, part) + 8 * (m & 1)));
+  const bf16x4 hi = ds_read_tr4((const bf16*)(v + v_at<bf16, D>(row + 16, part) + 8 * (m & 1)));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <int D>
+__device__ __forceinline__ f32x4 v_frag(const char* v, int c, int m, int g, float) {
+  f32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    r[e] = *(const float*)(v + v_at<float, D>(4 * g + e, 4 * c + (m >> 2)) + 4 * (m & 3));
+  return r;
+}
+__device__ __forceinline__ bf16x8 p_frag(const f32x4 (&s)[2], bf16) { return frag_from_acc(s[0], s[1], bf16()); }
+__device__ __forceinline__ f32x4 p_frag(const f32x4 (&s)[1], float) { return s[0]; }
+
+__device__ __forceinline__ bf16x8 finite(bf16x8 x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = nonfinite((float)x[i]) ? (bf16)0.f : x[i];
+  return x;
+}
+__device__ __forceinline__ f32x4 finite(f32x4 x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = nonfinite(x[i]) ? 0.f : x[i];
+  return x;
+}
+
+// Workspace: how the work is cut, then two partial results per workgroup (an item cut at its start
+// and one cut at its end), each 16 rows of D sums, then m and l of each row.
+struct Ws {
+  int64_t* split;  // [0]: units per workgroup, [1 + n]: first unit of sequence n, n = 0 .. num_seqs
+  float* part;
+};
+__host__ __device__ inline size_t split_bytes(int num_seqs) {
+  return ((size_t)(num_seqs + 2) * 8 + 255) / 256 * 256;
+}
+__host__ __device__ inline Ws ws_at(char* ws, int num_seqs) {
+  return {reinterpret_cast<int64_t*>(ws), reinterpret_cast<float*>(ws + split_bytes(num_seqs))};
+}
+constexpr int part_floats(int D) { return 16 * D + 32; }
+
+// Units of sequence n's items, all heads and tiles.
+__device__ __forceinline__ int64_t seq_units(const Seq& s, int Hk, int unit) {
+  return (int64_t)((s.rows + 15) / 16) * Hk * ((s.hi - s.lo + unit - 1) / unit);
+}
+
+template <typename MT, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArgs a) {
+  typedef Row<MT, D> R;
+  typedef typename R::frag frag;
+  constexpr int KS = R::KS, NG = R::NG, SK = R::SK, NC = R::NC, UNIT = R::UNIT;
+  __shared__ __align__(16) char lds[R::LDS];
+  __shared__ float ml[kWaves][16][2];
+  __shared__ int64_t scan[kWaves], found[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
+  const int N = a.b.num_seqs, Hk = a.num_kv_heads, G = a.num_q_heads / Hk, ps = a.b.page_size,
+            shift = __builtin_ctz(ps);
+  const Ws ws = ws_at(a.workspace, N);
+
+  // --- this workgroup's share [at, end) of all units: each thread adds up a run of sequences
+  const int run = (N + kThreads - 1) / kThreads, n0 = min(N, tid * run), n1 = min(N, n0 + run);
+  int64_t mine = 0;
+  for (int n = n0; n < n1; ++n) mine += seq_units(seq_at(a, n, G, UNIT), Hk, UNIT);
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t y = __shfl_up(incl, d);
+    if (lane >= d) incl += y;
   }
-  for (int e = 0; e < E; ++e)
-    ((T*)a.o)[(t * a.num_q_heads + hq) * D + e * 64 + threadIdx.x] = from_f32<T>(l > 0.f ? o[e] / l : l);
-  if (a.lse && threadIdx.x == 0) a.lse[t * a.num_q_heads + hq] = m + logf(l);
+  if (lane == 63) scan[wave] = incl;
+  __syncthreads();
+  int64_t total = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? scan[w] : 0;
+    total += scan[w];
+  }
+  const int64_t per = max((int64_t)1, (total + kGroups - 1) / kGroups);
+  if (blockIdx.x == 0) {
+    int64_t f = before;
+    for (int n = n0; n < n1; ++n) {
+      ws.split[1 + n] = f;
+      f += seq_units(seq_at(a, n, G, UNIT), Hk, UNIT);
+    }
+    if (tid == 0) ws.split[0] = per;
+    if (n0 < n1 && n1 == N) ws.split[1 + N] = f;
+  }
+  int64_t at = (int64_t)blockIdx.x * per;
+  const int64_t begin = at, end = min(total, at + per);
+  if (at >= end) return;
+  if (before <= at && at < before + mine) {
+    int64_t f = before;
+    int n = n0;
+    for (;; ++n) {
+      const int64_t u = seq_units(seq_at(a, n, G, UNIT), Hk, UNIT);
+      if (at < f + u) break;
+      f += u;
+    }
+    found[0] = n;
+    found[1] = f;
+  }
+  __syncthreads();
+  int n = (int)found[0];
+  int64_t first = found[1];  // first unit of sequence n
+
+  const float c = a.scale * LOG2E;
+  while (at < end) {
+    const Seq s = seq_at(a, n, G, UNIT);
+    const int units = (s.hi - s.lo + UNIT - 1) / UNIT, tiles = (s.rows + 15) / 16;
+    const int64_t all = (int64_t)tiles * Hk * units;
+    if (at >= first + all) {
+      first += all;
+      ++n;
+      continue;
+    }
+    const int item = (int)((at - first) / units), u0 = (int)((at - first) - (int64_t)item * units);
+    const int u1 = (int)min((int64_t)units, u0 + (end - at));
+    const int h = item / tiles, tile = item - h * tiles;
+
+    // --- the tile's rows: lane m's query, its visible keys
+    const int row = tile * 16 + m;
+    const bool has = row < s.rows;
+    const int tok = has ? row / G : 0, hq = h * G + (has ? row - tok * G : 0);
+    const int p = s.p0 + tok, phi = has ? min(p, s.hi - 1) : -1,
+              plo = a.window ? max(0, p - a.window + 1) : 0;
+    const MT* q = (const MT*)a.q + (s.row0 + tok) * a.q_stride + hq * D;
+    frag qf[SK];
+#pragma unroll
+    for (int i = 0; i < SK; ++i) {
+      qf[i] = *reinterpret_cast<const frag*>(q + KS * i + R::EPL * g);
+      if (!has) qf[i] = frag{};
+    }
+    // keys any_lo .. any_hi are seen by some row, full_lo .. full_hi by every row
+    int any_lo = has ? plo : INT32_MAX, any_hi = phi, full_lo = has ? plo : 0, full_hi = has ? phi : INT32_MAX;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+      any_lo = min(any_lo, __shfl_xor(any_lo, d));
+      any_hi = max(any_hi, __shfl_xor(any_hi, d));
+      full_lo = max(full_lo, __shfl_xor(full_lo, d));
+      full_hi = min(full_hi, __shfl_xor(full_hi, d));
+    }
+    any_lo = __builtin_amdgcn_readfirstlane(any_lo);
+    any_hi = __builtin_amdgcn_readfirstlane(any_hi);
+    full_lo = __builtin_amdgcn_readfirstlane(full_lo);
+    full_hi = __builtin_amdgcn_readfirstlane(full_hi);
+
+    const int32_t* table = a.b.block_table + n * a.b.table_stride;
+    const int64_t head = (int64_t)h * ps * D;
+    const int key0 = s.lo + u0 * UNIT + wave * KS, nb = u1 - u0;  // the wave's blocks: key0 + i UNIT
+    char* vl = lds + wave * R::TILE;
+
+    f32x4 acc[NC] = {};
+    float mx = -INFINITY, sum = 0.f;
+    v4u32 kr[NG * SK], vr[R::VL];
+    int pg[NG], pgn[NG];  // pages of the block in registers and of the one after it; -1: none
+
+    auto pages = [&](int i, int (&e)[NG]) {
+#pragma unroll
+      for (int t = 0; t < NG; ++t) {
+        const int key = key0 + i * UNIT + 16 * t;
+        int x = -1;
+        if (i < nb && key < s.hi) x = table[key >> shift];
+        x = __builtin_amdgcn_readfirstlane(x);
+        e[t] = page_ok(x, a.b.num_pages) ? x : -1;
+      }
+    };
+    auto load_k = [&](int i, const int (&e)[NG]) {
+#pragma unroll
+      for (int t = 0; t < NG; ++t) {
+        const int key = key0 + i * UNIT + 16 * t;
+        const MT* k = (const MT*)a.k_pages + max(e[t], 0) * a.k_page_stride + head + (key & (ps - 1)) * D;
+#pragma unroll
+        for (int j = 0; j < SK; ++j)
+          kr[t * SK + j] = *reinterpret_cast<const v4u32*>(k + m * D + KS * j + R::EPL * g);
+      }
+    };
+    auto load_v = [&](int i, const int (&e)[NG]) {
+#pragma unroll
+      for (int t = 0; t < NG; ++t) {
+        const int key = key0 + i * UNIT + 16 * t;
+        const MT* v = (const MT*)a.v_pages + max(e[t], 0) * a.v_page_stride + head + (key & (ps - 1)) * D;
+#pragma unroll
+        for (int j = 0; j < R::VL / NG; ++j)
+          vr[t * (R::VL / NG) + j] = *reinterpret_cast<const v4u32*>(v + (j * 64 + lane) * (16 / R::ES));
+      }
+    };
+    pages(0, pg);
+    pages(1, pgn);
+    if (nb > 0) {
+      load_k(0, pg);
+      load_v(0, pg);
+    }
+    for (int i = 0; i < nb; ++i) {
+      const int kb = key0 + i * UNIT;
+      bool whole = kb >= full_lo && kb + KS - 1 <= full_hi;
+#pragma unroll
+      for (int t = 0; t < NG; ++t) whole = whole && pg[t] >= 0;
+      // --- scores
+      f32x4 st[NG] = {};
+#pragma unroll
+      for (int t = 0; t < NG; ++t)
+#pragma unroll
+        for (int j = 0; j < SK; ++j)
+          st[t] = Mma<MT>::mma(__builtin_bit_cast(frag, kr[t * SK + j]), qf[j], st[t]);
+      // --- values to LDS; those that no row sees as zeros
+      bool odd = false;
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < R::VL; ++j) {
+          const int r = j * R::RPI + lane / R::RC, key = kb + r;
+          if (key < any_lo || key > any_hi || pg[j * R::RPI / 16] < 0) vr[j] = v4u32{0, 0, 0, 0};
+          odd |= any_nonfinite<MT>(vr[j]);
+        }
+        odd = __any(odd);
+      }
+#pragma unroll
+      for (int j = 0; j < R::VL; ++j)
+        *reinterpret_cast<v4u32*>(vl + v_at<MT, D>(j * R::RPI + lane / R::RC, lane % R::RC)) = vr[j];
+      // --- the next block is on its way while this one is computed
+      int pc[NG];
+#pragma unroll
+      for (int t = 0; t < NG; ++t) pc[t] = pg[t], pg[t] = pgn[t];
+      if (i + 1 < nb) {
+        pages(i + 2, pgn);
+        load_k(i + 1, pg);
+        load_v(i + 1, pg);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int t = 0; t < NG; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = kb + 16 * t + 4 * g + r;
+            if (key < plo || key > phi || pc[t] < 0) st[t][r] = -INFINITY;
+          }
+      }
+      // --- running maximum and sum
+      float tm = st[0][0];
+#pragma unroll
+      for (int t = 0; t < NG; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tm = fmaxf(tm, st[t][r]);
+      tm = across32(across16(tm, MaxOp()), MaxOp());
+      if (__any(tm > mx)) {
+        const float mn = fmaxf(mx, tm), al = exp2_f((mx - (mn == -INFINITY ? 0.f : mn)) * c);
+        sum *= al;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) acc[j] *= al;
+        mx = mn;
+      }
+      const float mc = mx == -INFINITY ? 0.f : mx * c;
+#pragma unroll
+      for (int t = 0; t < NG; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          st[t][r] = exp2_f(fmaf(st[t][r], c, -mc));
+          sum += st[t][r];
+        }
+      // --- O^T += V^T P^T
+      const frag pf = p_frag(st, MT());
+      if (!odd) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) acc[j] = Mma<MT>::mma(v_frag<D>(vl, j, m, g, MT()), pf, acc[j]);
+      } else {
+        // An infinity or NaN in a key's values, which some row may not see: it counts as 0 in the
+        // product, and is added to the rows that do see it.
+#pragma unroll
+        for (int j = 0; j < NC; ++j) acc[j] = Mma<MT>::mma(finite(v_frag<D>(vl, j, m, g, MT())), pf, acc[j]);
+#pragma unroll
+        for (int t = 0; t < NG; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll 1
+            for (int gg = 0; gg < 4; ++gg) {
+              const float w = __shfl(st[t][r], 16 * gg + m);
+              const int kr_ = 16 * t + 4 * gg + r, key = kb + kr_;
+              if (key < plo || key > phi) continue;
+#pragma unroll
+              for (int j = 0; j < NC; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const int ch = 16 * j + 4 * g + x, per16 = 16 / R::ES;
+                  const float v = (float)*(const MT*)(vl + v_at<MT, D>(kr_, ch / per16) + ch % per16 * R::ES);
+                  if (nonfinite(v)) acc[j][x] += w * v;
+                }
+            }
+      }
+    }
+    sum = across32(across16(sum, SumOp()), SumOp());
+
+    // --- the waves meet: weights of their maxima, sums of their outputs
+    __syncthreads();
+    if (g == 0) ml[wave][m][0] = mx, ml[wave][m][1] = sum;
+    float* ot = reinterpret_cast<float*>(lds) + wave * 16 * D;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)  // parts of 16 bytes permuted by row: lanes of a column differ in bank
+      *reinterpret_cast<f32x4*>(ot + m * D + 4 * ((4 * j + g) ^ (m & 7))) = acc[j];
+    __syncthreads();
+    const bool done = u0 == 0 && u1 == units;
+    float* part = ws.part + (2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1)) * part_floats(D);
+#pragma unroll
+    for (int e = 0; e < 16 * D / 4 / kThreads; ++e) {
+      const int i = e * kThreads + tid, r = i / (D / 4), q4 = i % (D / 4), orow = tile * 16 + r;
+      float M = ml[0][r][0];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) M = fmaxf(M, ml[w][r][0]);
+      const float Mu = M == -INFINITY ? 0.f : M;
+      f32x4 o = {};
+      float l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float al = exp2_f((ml[w][r][0] - Mu) * c);
+        l += al * ml[w][r][1];
+        o += al * *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds) + (w * 16 + r) * D + 4 * (q4 ^ (r & 7)));
+      }
+      if (orow >= s.rows) continue;
+      if (done) {
+        const int ti = orow / G, hh = h * G + orow - ti * G;
+        const int64_t out = (s.row0 + ti) * a.num_q_heads + hh;
+        o *= l == 0.f ? 0.f : 1.f / l;
+        MT* dst = (MT*)a.o + out * D + 4 * q4;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) dst[x] = from_f32<MT>(o[x]);
+        if (a.lse && q4 == 0) a.lse[out] = M * a.scale + (l == 0.f ? 0.f : logf(l));
+      } else {
+        *reinterpret_cast<f32x4*>(part + r * D + 4 * q4) = o;
+        if (q4 == 0) part[16 * D + 2 * r] = M, part[16 * D + 2 * r + 1] = l;
+      }
+    }
+    __syncthreads();
+    at += u1 - u0;
+  }
+}
+
+// Joins the parts of items that were cut, and writes the rows that have no keys: one wave per
+// (token, query head).
+template <typename MT, int D>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
+  typedef Row<MT, D> R;
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63, N = a.b.num_seqs, Hk = a.num_kv_heads, G = a.num_q_heads / Hk;
+  const int64_t out = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  if (out >= a.b.total_tokens * a.num_q_heads) return;
+  const int64_t t = out / a.num_q_heads;
+  const int hq = (int)(out - t * a.num_q_heads), h = hq / G;
+  // the token's sequence: the boundaries at or below it, counted over the lanes
+  int n = 0;
+  if (a.b.cu_seqlens) {
+    for (int i = lane; i < N; i += 64) n += first_row(a.b, i + 1) <= t;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+    if (n == N || t < first_row(a.b, 0)) return;
+  } else {
+    n = (int)(t / (a.b.total_tokens / N));
+  }
+  const Ws ws = ws_at(a.workspace, N);
+  const Seq s = seq_at(a, n, G, R::UNIT);
+  const int units = (s.hi - s.lo + R::UNIT - 1) / R::UNIT, row = (int)(t - s.row0) * G + hq - h * G;
+  float o[E] = {}, M = -INFINITY, l = 0.f;
+  if (units > 0) {
+    const int64_t per = ws.split[0];
+    const int64_t b = ws.split[1 + n] + ((int64_t)h * ((s.rows + 15) / 16) + row / 16) * units, e = b + units;
+    const int64_t w0 = b / per, w1 = (e - 1) / per;
+    if (w0 == w1) return;
+    for (int64_t w = w0; w <= w1; ++w) {
+      const float* part = ws.part + (2 * w + (w == w0 && b != w * per)) * part_floats(D);
+      const float pm = part[16 * D + 2 * (row & 15)], pl = part[16 * D + 2 * (row & 15) + 1];
+      const float mn = fmaxf(M, pm), mu = mn == -INFINITY ? 0.f : mn;
+      const float c = a.scale * LOG2E, al = exp2_f((M - mu) * c), be = exp2_f((pm - mu) * c);
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = o[i] * al + be * part[(row & 15) * D + E * lane + i];
+      l = l * al + be * pl;
+      M = mn;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < E; ++i) ((MT*)a.o)[out * D + E * lane + i] = from_f32<MT>(o[i] * inv);
+  if (a.lse && lane == 0) a.lse[out] = M * a.scale + (l == 0.f ? 0.f : logf(l));
+}
+
+template <typename MT, int D>
+void launch_rows(const AttnArgs& a) {
+  row_kernel<MT, D><<<kGroups, kThreads, 0, a.stream>>>(a);
+  const int64_t rows = a.b.total_tokens * a.num_q_heads;
+  join_kernel<MT, D><<<(unsigned)((rows + kWaves - 1) / kWaves), kThreads, 0, a.stream>>>(a);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int, int64_t, int, int, int, bool) { return 256; }
+size_t attn_workspace_bytes(int num_seqs, int64_t, int, int, int head_dim, bool) {
+  return split_bytes(num_seqs) + (size_t)2 * kGroups * part_floats(head_dim) * 4;
+}
 
 hipError_t launch_attn(const AttnArgs& a) {
-  const unsigned g = (unsigned)(a.b.total_tokens * a.num_q_heads);
-  if (g == 0) return hipSuccess;
+  if (a.b.total_tokens == 0) return hipSuccess;
   if (a.dtype_bf16) {
-    if (a.head_dim == 64) attn_kernel<bf16, 64><<<g, 64, 0, a.stream>>>(a);
-    if (a.head_dim == 128) attn_kernel<bf16, 128><<<g, 64, 0, a.stream>>>(a);
-    if (a.head_dim == 256) attn_kernel<bf16, 256><<<g, 64, 0, a.stream>>>(a);
+    if (a.head_dim == 64) launch_rows<bf16, 64>(a);
+    if (a.head_dim == 128) launch_rows<bf16, 128>(a);
+    if (a.head_dim == 256) launch_rows<bf16, 256>(a);
   } else {
-    if (a.head_dim == 64) attn_kernel<float, 64><<<g, 64, 0, a.stream>>>(a);
-    if (a.head_dim == 128) attn_kernel<float, 128><<<g, 64, 0, a.stream>>>(a);
-    if (a.head_dim == 256) attn_kernel<float, 256><<<g, 64, 0, a.stream>>>(a);
+    if (a.head_dim == 64) launch_rows<float, 64>(a);
+    if (a.head_dim == 128) launch_rows<float, 128>(a);
+    if (a.head_dim == 256) launch_rows<float, 256>(a);
   }
   return hipGetLastError();
 }
