@@ -17,7 +17,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_scan.hip", "kda_bwd.hip",
            "kda_wide.hip", "kda_noalloc.hip", "kda_prologue.hip", "kda_paged_api.cpp",
-           "kda_rope.hip", "kda_attn.hip", "kda_pages.hip"]
+           "kda_rope.hip", "kda_attn.hip", "kda_attn_tile.hip", "kda_pages.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

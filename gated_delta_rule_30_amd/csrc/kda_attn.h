@@ -56,6 +56,9 @@ struct SumOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
 
+// A float that was stored as part of 16 bytes of unsigned words.
+typedef float __attribute__((may_alias)) lds_float;
+
 // A page's first element of one K/V head; entry < 0 or past the pool names no page, and page 0
 // stands in for it, whose rows are then masked.
 __device__ __forceinline__ bool page_ok(int entry, int num_pages) { return (unsigned)entry < (unsigned)num_pages; }
@@ -75,11 +78,85 @@ template <> __device__ __forceinline__ bool any_nonfinite<bf16>(v4u32 x) {
     r |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
   return r;
 }
-__device__ __forceinline__ bool nonfinite(float x) {
-  return (__builtin_bit_cast(unsigned, x) & 0x7f800000u) == 0x7f800000u;
+// 16 bytes of elements, infinities and NaN as 0.
+template <typename T> __device__ __forceinline__ v4u32 finite_part(v4u32 x);
+template <> __device__ __forceinline__ v4u32 finite_part<float>(v4u32 x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = (x[i] & 0x7f800000u) == 0x7f800000u ? 0u : x[i];
+  return x;
+}
+template <> __device__ __forceinline__ v4u32 finite_part<bf16>(v4u32 x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    x[i] &= ((x[i] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((x[i] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+  return x;
+}
+// PART 0: x, an infinity or NaN as 0; 1: 1 for +inf or NaN, else 0; 2: 1 for -inf or NaN, else 0.
+template <int PART>
+__device__ __forceinline__ float odd_part(float x) {
+  const bool odd = (__builtin_bit_cast(unsigned, x) & 0x7f800000u) == 0x7f800000u;
+  if constexpr (PART == 0) return odd ? 0.f : x;
+  return odd && x != (PART == 1 ? -INFINITY : INFINITY) ? 1.f : 0.f;
+}
+template <int PART>
+__device__ __forceinline__ bf16x8 odd_part(bf16x8 x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (bf16)odd_part<PART>((float)x[i]);
+  return x;
+}
+template <int PART>
+__device__ __forceinline__ f32x4 odd_part(f32x4 x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = odd_part<PART>(x[i]);
+  return x;
 }
 
-constexpr float LN2 = 0.6931471805599453f;
+// ------------------------------------------------------------------ the tile kernel's plan
+// Sequences of more than row_limit rows go to the tile kernel (kda_attn_tile.hip), in tiles of
+// tile_rows rows. The plan numbers the tiles of all sequences, sequence n's from tile_first[n],
+// and adds up their units (32 keys): pre[i] are those of the tiles before tile i, for one K/V
+// head. All heads' units are laid end to end by (sequence, head, tile): sequence n starts at
+// Hk pre[tile_first[n]].
+constexpr int kTileUnit = 32;
+constexpr int kTileGroups = 256;  // workgroups of the tile kernel: one per compute unit
+// Rows of a tile: 64 per wave where their sums fit the registers, else 32.
+constexpr int attn_tile_rows(int D, bool bf16) { return bf16 && D <= 128 ? 256 : 128; }
 
+struct TilePlan {
+  int64_t *pre, *tile_first;
+  float* part;  // two partial results per workgroup: tile_rows rows of D sums, then m and l of each
+};
+__host__ __device__ inline int64_t max_tiles(int num_seqs, int64_t total_tokens, int G, int tile_rows) {
+  return total_tokens * G / tile_rows + num_seqs;
+}
+__host__ __device__ inline size_t tile_plan_bytes(int num_seqs, int64_t tiles) {
+  return ((size_t)(tiles + 1 + num_seqs + 1) * 8 + 255) / 256 * 256;
+}
+__host__ __device__ inline TilePlan tile_plan_at(char* ws, int num_seqs, int64_t tiles) {
+  TilePlan p;
+  p.tile_first = reinterpret_cast<int64_t*>(ws);
+  p.pre = p.tile_first + num_seqs + 1;
+  p.part = reinterpret_cast<float*>(ws + tile_plan_bytes(num_seqs, tiles));
+  return p;
+}
+__host__ __device__ constexpr int64_t tile_part_floats(int rows, int D) { return (int64_t)rows * D + 2 * rows; }
+
+// Keys lo .. hi - 1 that some row of a sequence's tile sees (lo a multiple of the unit).
+struct TileKeys {
+  int lo, hi, units;
+};
+__device__ __forceinline__ TileKeys tile_keys(const AttnArgs& a, const Seq& s, int tile, int G) {
+  const int i0 = (int)((int64_t)tile * a.tile_rows / G);
+  const int i1 = (int)((min((int64_t)(tile + 1) * a.tile_rows, (int64_t)s.rows) - 1) / G);
+  TileKeys k;
+  k.hi = (int)min((int64_t)s.hi, (int64_t)s.p0 + i1 + 1);
+  const int64_t lo = a.window ? (int64_t)s.p0 + i0 - a.window + 1 : 0;
+  k.lo = lo > 0 ? (int)(min(lo, (int64_t)INT32_MAX) / kTileUnit) * kTileUnit : 0;
+  k.units = k.hi > k.lo ? (k.hi - k.lo + kTileUnit - 1) / kTileUnit : 0;
+  return k;
+}
+
+void launch_attn_tile(const AttnArgs& a);
+size_t attn_tile_bytes(int num_seqs, int64_t total_tokens, int G, int head_dim, int tile_rows);
 
 }  // namespace kda

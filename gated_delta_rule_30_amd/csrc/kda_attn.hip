@@ -64,22 +64,11 @@ __device__ __forceinline__ f32x4 v_frag(const char* v, int c, int m, int g, floa
   f32x4 r;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    r[e] = *(const float*)(v + v_at<float, D>(4 * g + e, 4 * c + (m >> 2)) + 4 * (m & 3));
+    r[e] = *(const lds_float*)(v + v_at<float, D>(4 * g + e, 4 * c + (m >> 2)) + 4 * (m & 3));
   return r;
 }
 __device__ __forceinline__ bf16x8 p_frag(const f32x4 (&s)[2], bf16) { return frag_from_acc(s[0], s[1], bf16()); }
 __device__ __forceinline__ f32x4 p_frag(const f32x4 (&s)[1], float) { return s[0]; }
-
-__device__ __forceinline__ bf16x8 finite(bf16x8 x) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = nonfinite((float)x[i]) ? (bf16)0.f : x[i];
-  return x;
-}
-__device__ __forceinline__ f32x4 finite(f32x4 x) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = nonfinite(x[i]) ? 0.f : x[i];
-  return x;
-}
 
 // Workspace: how the work is cut, then two partial results per workgroup (an item cut at its start
 // and one cut at its end), each 16 rows of D sums, then m and l of each row.
@@ -95,8 +84,9 @@ __host__ __device__ inline Ws ws_at(char* ws, int num_seqs) {
 }
 constexpr int part_floats(int D) { return 16 * D + 32; }
 
-// Units of sequence n's items, all heads and tiles.
-__device__ __forceinline__ int64_t seq_units(const Seq& s, int Hk, int unit) {
+// Units of sequence n's items, all heads and tiles; none if the tile kernel takes it.
+__device__ __forceinline__ int64_t seq_units(const AttnArgs& a, const Seq& s, int Hk, int unit) {
+  if (s.rows > a.row_limit) return 0;
   return (int64_t)((s.rows + 15) / 16) * Hk * ((s.hi - s.lo + unit - 1) / unit);
 }
 
@@ -116,7 +106,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
   // --- this workgroup's share [at, end) of all units: each thread adds up a run of sequences
   const int run = (N + kThreads - 1) / kThreads, n0 = min(N, tid * run), n1 = min(N, n0 + run);
   int64_t mine = 0;
-  for (int n = n0; n < n1; ++n) mine += seq_units(seq_at(a, n, G, UNIT), Hk, UNIT);
+  for (int n = n0; n < n1; ++n) mine += seq_units(a, seq_at(a, n, G, UNIT), Hk, UNIT);
   int64_t incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -136,7 +126,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
     int64_t f = before;
     for (int n = n0; n < n1; ++n) {
       ws.split[1 + n] = f;
-      f += seq_units(seq_at(a, n, G, UNIT), Hk, UNIT);
+      f += seq_units(a, seq_at(a, n, G, UNIT), Hk, UNIT);
     }
     if (tid == 0) ws.split[0] = per;
     if (n0 < n1 && n1 == N) ws.split[1 + N] = f;
@@ -148,7 +138,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
     int64_t f = before;
     int n = n0;
     for (;; ++n) {
-      const int64_t u = seq_units(seq_at(a, n, G, UNIT), Hk, UNIT);
+      const int64_t u = seq_units(a, seq_at(a, n, G, UNIT), Hk, UNIT);
       if (at < f + u) break;
       f += u;
     }
@@ -163,7 +153,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
   while (at < end) {
     const Seq s = seq_at(a, n, G, UNIT);
     const int units = (s.hi - s.lo + UNIT - 1) / UNIT, tiles = (s.rows + 15) / 16;
-    const int64_t all = (int64_t)tiles * Hk * units;
+    const int64_t all = seq_units(a, s, Hk, UNIT);
     if (at >= first + all) {
       first += all;
       ++n;
@@ -318,28 +308,30 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
 #pragma unroll
         for (int j = 0; j < NC; ++j) acc[j] = Mma<MT>::mma(v_frag<D>(vl, j, m, g, MT()), pf, acc[j]);
       } else {
-        // An infinity or NaN in a key's values, which some row may not see: it counts as 0 in the
-        // product, and is added to the rows that do see it.
-#pragma unroll
-        for (int j = 0; j < NC; ++j) acc[j] = Mma<MT>::mma(finite(v_frag<D>(vl, j, m, g, MT())), pf, acc[j]);
+        // An infinity or NaN in a value, which a weight of 0 does not hide: it counts as 0 in the
+        // product; then rows that see a key whose value is +inf or NaN gain +inf, rows that see -inf or
+        // NaN gain -inf, so that NaN or both make NaN.
+        f32x4 vt[NG];
 #pragma unroll
         for (int t = 0; t < NG; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll 1
-            for (int gg = 0; gg < 4; ++gg) {
-              const float w = __shfl(st[t][r], 16 * gg + m);
-              const int kr_ = 16 * t + 4 * gg + r, key = kb + kr_;
-              if (key < plo || key > phi) continue;
+          for (int r = 0; r < 4; ++r) {
+            const int key = kb + 16 * t + 4 * g + r;
+            vt[t][r] = key < plo || key > phi ? 0.f : 1.f;
+          }
+        const frag vis = p_frag(vt, MT());
 #pragma unroll
-              for (int j = 0; j < NC; ++j)
+        for (int j = 0; j < NC; ++j) {
+          const frag f = v_frag<D>(vl, j, m, g, MT());
+          acc[j] = Mma<MT>::mma(odd_part<0>(f), pf, acc[j]);
+          const f32x4 pos = Mma<MT>::mma(odd_part<1>(f), vis, f32x4{});
+          const f32x4 neg = Mma<MT>::mma(odd_part<2>(f), vis, f32x4{});
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const int ch = 16 * j + 4 * g + x, per16 = 16 / R::ES;
-                  const float v = (float)*(const MT*)(vl + v_at<MT, D>(kr_, ch / per16) + ch % per16 * R::ES);
-                  if (nonfinite(v)) acc[j][x] += w * v;
-                }
-            }
+          for (int x = 0; x < 4; ++x) {
+            if (pos[x] > 0.f) acc[j][x] += INFINITY;
+            if (neg[x] > 0.f) acc[j][x] -= INFINITY;
+          }
+        }
       }
     }
     sum = across32(across16(sum, SumOp()), SumOp());
@@ -409,22 +401,40 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
   } else {
     n = (int)(t / (a.b.total_tokens / N));
   }
-  const Ws ws = ws_at(a.workspace, N);
+  // its item: units b .. e - 1 of the kernel that computed it, in shares of `per`
   const Seq s = seq_at(a, n, G, R::UNIT);
-  const int units = (s.hi - s.lo + R::UNIT - 1) / R::UNIT, row = (int)(t - s.row0) * G + hq - h * G;
+  const int row = (int)(t - s.row0) * G + hq - h * G;
+  int64_t per, b, e;
+  const float* parts;
+  int64_t size;
+  int r, rows;  // the row within its tile, and the tile's rows
+  if (s.rows > a.row_limit) {
+    const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, a.tile_rows));
+    const int64_t t0 = pl.tile_first[n], i = t0 + row / a.tile_rows;
+    per = max((int64_t)1, (Hk * pl.pre[pl.tile_first[N]] + kTileGroups - 1) / kTileGroups);
+    b = Hk * pl.pre[t0] + h * (pl.pre[pl.tile_first[n + 1]] - pl.pre[t0]) + pl.pre[i] - pl.pre[t0];
+    e = b + pl.pre[i + 1] - pl.pre[i];
+    parts = pl.part, rows = a.tile_rows, size = tile_part_floats(rows, D), r = row % rows;
+  } else {
+    const Ws ws = ws_at(a.workspace, N);
+    const int units = (s.hi - s.lo + R::UNIT - 1) / R::UNIT;
+    per = ws.split[0];
+    b = ws.split[1 + n] + ((int64_t)h * ((s.rows + 15) / 16) + row / 16) * units;
+    e = b + units;
+    parts = ws.part, rows = 16, size = part_floats(D), r = row & 15;
+  }
   float o[E] = {}, M = -INFINITY, l = 0.f;
-  if (units > 0) {
-    const int64_t per = ws.split[0];
-    const int64_t b = ws.split[1 + n] + ((int64_t)h * ((s.rows + 15) / 16) + row / 16) * units, e = b + units;
+  if (e > b) {
     const int64_t w0 = b / per, w1 = (e - 1) / per;
-    if (w0 == w1) return;
+    if (w0 == w1) return;  // written by its one workgroup
+    const float c = a.scale * LOG2E;
     for (int64_t w = w0; w <= w1; ++w) {
-      const float* part = ws.part + (2 * w + (w == w0 && b != w * per)) * part_floats(D);
-      const float pm = part[16 * D + 2 * (row & 15)], pl = part[16 * D + 2 * (row & 15) + 1];
+      const float* part = parts + (2 * w + (w == w0 && b != w * per)) * size;
+      const float pm = part[rows * D + 2 * r], pl = part[rows * D + 2 * r + 1];
       const float mn = fmaxf(M, pm), mu = mn == -INFINITY ? 0.f : mn;
-      const float c = a.scale * LOG2E, al = exp2_f((M - mu) * c), be = exp2_f((pm - mu) * c);
+      const float al = exp2_f((M - mu) * c), be = exp2_f((pm - mu) * c);
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = o[i] * al + be * part[(row & 15) * D + E * lane + i];
+      for (int i = 0; i < E; ++i) o[i] = o[i] * al + be * part[(int64_t)r * D + E * lane + i];
       l = l * al + be * pl;
       M = mn;
     }
@@ -435,29 +445,65 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
   if (a.lse && lane == 0) a.lse[out] = M * a.scale + (l == 0.f ? 0.f : logf(l));
 }
 
+// Which kernel takes which sequence. Without cu_seqlens every sequence has the same rows; with
+// it and no more tokens than sequences, the batch is one of decode steps.
+struct Route {
+  int row_limit, tile_rows;  // tile_rows 0: no tile kernel
+  bool rows;                 // whether the row kernel runs
+};
+constexpr int kRowLimit = 32;
+Route route(int num_seqs, int64_t total_tokens, int G, bool ragged, int tile_rows) {
+  const int64_t rows = total_tokens / num_seqs * G;
+  Route r = {INT32_MAX, 0, true};
+  if (ragged ? total_tokens > num_seqs : rows > kRowLimit) {
+    r.row_limit = kRowLimit;
+    r.rows = ragged;
+    r.tile_rows = tile_rows;
+  }
+  return r;
+}
+
 template <typename MT, int D>
-void launch_rows(const AttnArgs& a) {
-  row_kernel<MT, D><<<kGroups, kThreads, 0, a.stream>>>(a);
-  const int64_t rows = a.b.total_tokens * a.num_q_heads;
-  join_kernel<MT, D><<<(unsigned)((rows + kWaves - 1) / kWaves), kThreads, 0, a.stream>>>(a);
+void launch_rows(const AttnArgs& a, bool rows) {
+  if (rows) row_kernel<MT, D><<<kGroups, kThreads, 0, a.stream>>>(a);
+  if (a.tile_rows) launch_attn_tile(a);
+  const int64_t n = a.b.total_tokens * a.num_q_heads;
+  join_kernel<MT, D><<<(unsigned)((n + kWaves - 1) / kWaves), kThreads, 0, a.stream>>>(a);
+}
+
+size_t row_bytes(int num_seqs, int head_dim) {
+  return (split_bytes(num_seqs) + (size_t)2 * kGroups * part_floats(head_dim) * 4 + 255) / 256 * 256;
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int num_seqs, int64_t, int, int, int head_dim, bool) {
-  return split_bytes(num_seqs) + (size_t)2 * kGroups * part_floats(head_dim) * 4;
+size_t attn_workspace_bytes(int num_seqs, int64_t total_tokens, int num_q_heads, int num_kv_heads,
+                            int head_dim, bool bf16) {
+  const int G = num_q_heads / num_kv_heads;
+  size_t tile = 0;
+  for (int ragged = 0; ragged < 2; ++ragged) {
+    const Route r = route(num_seqs, total_tokens, G, ragged, attn_tile_rows(head_dim, bf16));
+    const size_t n = r.tile_rows ? attn_tile_bytes(num_seqs, total_tokens, G, head_dim, r.tile_rows) : 0;
+    tile = n > tile ? n : tile;
+  }
+  return row_bytes(num_seqs, head_dim) + tile;
 }
 
-hipError_t launch_attn(const AttnArgs& a) {
-  if (a.b.total_tokens == 0) return hipSuccess;
+hipError_t launch_attn(const AttnArgs& args) {
+  if (args.b.total_tokens == 0) return hipSuccess;
+  AttnArgs a = args;
+  const Route r = route(a.b.num_seqs, a.b.total_tokens, a.num_q_heads / a.num_kv_heads, a.b.cu_seqlens != nullptr,
+                        attn_tile_rows(a.head_dim, a.dtype_bf16));
+  a.row_limit = r.row_limit, a.tile_rows = r.tile_rows;
+  a.tile_ws = a.workspace + row_bytes(a.b.num_seqs, a.head_dim);
   if (a.dtype_bf16) {
-    if (a.head_dim == 64) launch_rows<bf16, 64>(a);
-    if (a.head_dim == 128) launch_rows<bf16, 128>(a);
-    if (a.head_dim == 256) launch_rows<bf16, 256>(a);
+    if (a.head_dim == 64) launch_rows<bf16, 64>(a, r.rows);
+    if (a.head_dim == 128) launch_rows<bf16, 128>(a, r.rows);
+    if (a.head_dim == 256) launch_rows<bf16, 256>(a, r.rows);
   } else {
-    if (a.head_dim == 64) launch_rows<float, 64>(a);
-    if (a.head_dim == 128) launch_rows<float, 128>(a);
-    if (a.head_dim == 256) launch_rows<float, 256>(a);
+    if (a.head_dim == 64) launch_rows<float, 64>(a, r.rows);
+    if (a.head_dim == 128) launch_rows<float, 128>(a, r.rows);
+    if (a.head_dim == 256) launch_rows<float, 256>(a, r.rows);
   }
   return hipGetLastError();
 }

@@ -50,6 +50,10 @@ struct AttnArgs {
   float* lse;
   char* workspace;
   hipStream_t stream;
+  // set by launch_attn: sequences of more rows (new tokens x query heads per K/V head) than row_limit are
+  // computed in tiles of tile_rows rows, with their plan at tile_ws
+  int row_limit, tile_rows;
+  char* tile_ws;
 };
 size_t attn_workspace_bytes(int num_seqs, int64_t total_tokens, int num_q_heads, int num_kv_heads,
                             int head_dim, bool bf16);
