@@ -52,6 +52,18 @@ __device__ __forceinline__ float across16(float x, F f) {
 struct MaxOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
+// Largest of three in one instruction (fmaxf would first quiet each operand's NaN).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ __forceinline__ float across32_max(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const float a = __builtin_bit_cast(float, (unsigned)r[0]), b = __builtin_bit_cast(float, (unsigned)r[1]);
+  return max3(a, b, b);
+}
 struct SumOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
@@ -118,9 +130,26 @@ __device__ __forceinline__ f32x4 odd_part(f32x4 x) {
 // head. All heads' units are laid end to end by (sequence, head, tile): sequence n starts at
 // Hk pre[tile_first[n]].
 constexpr int kTileUnit = 32;
-constexpr int kTileGroups = 256;  // workgroups of the tile kernel: one per compute unit
-// Rows of a tile: 64 per wave where their sums fit the registers, else 32.
-constexpr int attn_tile_rows(int D, bool bf16) { return bf16 && D <= 128 ? 256 : 128; }
+
+// A workgroup's waves (of 32 rows each), the waves per SIMD that its registers allow,
+// and the workgroups: as many as the chip holds at once.
+template <int D, bool BF16>
+struct TileShape {
+  static constexpr int WAVES = BF16 && D <= 128 ? 8 : 4, PER_SIMD = D <= 128 ? 2 : 1;
+  static constexpr int ROWS = 32 * WAVES, GROUPS = 256 * 4 * PER_SIMD / WAVES;
+};
+template <typename F>
+constexpr int attn_tile_shape(int D, bool bf16, F f) {
+  return D == 64    ? (bf16 ? f(TileShape<64, true>()) : f(TileShape<64, false>()))
+         : D == 128 ? (bf16 ? f(TileShape<128, true>()) : f(TileShape<128, false>()))
+                    : (bf16 ? f(TileShape<256, true>()) : f(TileShape<256, false>()));
+}
+constexpr int attn_tile_rows(int D, bool bf16) {
+  return attn_tile_shape(D, bf16, [](auto s) { return decltype(s)::ROWS; });
+}
+constexpr int attn_tile_groups(int D, bool bf16) {
+  return attn_tile_shape(D, bf16, [](auto s) { return decltype(s)::GROUPS; });
+}
 
 struct TilePlan {
   int64_t *pre, *tile_first;
@@ -157,6 +186,6 @@ __device__ __forceinline__ TileKeys tile_keys(const AttnArgs& a, const Seq& s, i
 }
 
 void launch_attn_tile(const AttnArgs& a);
-size_t attn_tile_bytes(int num_seqs, int64_t total_tokens, int G, int head_dim, int tile_rows);
+size_t attn_tile_bytes(int num_seqs, int64_t total_tokens, int G, int head_dim, bool bf16);
 
 }  // namespace kda

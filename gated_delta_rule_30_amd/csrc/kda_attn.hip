@@ -411,7 +411,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
   if (s.rows > a.row_limit) {
     const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, a.tile_rows));
     const int64_t t0 = pl.tile_first[n], i = t0 + row / a.tile_rows;
-    per = max((int64_t)1, (Hk * pl.pre[pl.tile_first[N]] + kTileGroups - 1) / kTileGroups);
+    per = max((int64_t)1, (Hk * pl.pre[pl.tile_first[N]] + TileShape<D, sizeof(MT) == 2>::GROUPS - 1) / TileShape<D, sizeof(MT) == 2>::GROUPS);
     b = Hk * pl.pre[t0] + h * (pl.pre[pl.tile_first[n + 1]] - pl.pre[t0]) + pl.pre[i] - pl.pre[t0];
     e = b + pl.pre[i + 1] - pl.pre[i];
     parts = pl.part, rows = a.tile_rows, size = tile_part_floats(rows, D), r = row % rows;
@@ -483,7 +483,7 @@ size_t attn_workspace_bytes(int num_seqs, int64_t total_tokens, int num_q_heads,
   size_t tile = 0;
   for (int ragged = 0; ragged < 2; ++ragged) {
     const Route r = route(num_seqs, total_tokens, G, ragged, attn_tile_rows(head_dim, bf16));
-    const size_t n = r.tile_rows ? attn_tile_bytes(num_seqs, total_tokens, G, head_dim, r.tile_rows) : 0;
+    const size_t n = r.tile_rows ? attn_tile_bytes(num_seqs, total_tokens, G, head_dim, bf16) : 0;
     tile = n > tile ? n : tile;
   }
   return row_bytes(num_seqs, head_dim) + tile;

@@ -24,22 +24,24 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4;
 constexpr int SUB = kTileUnit;  // keys of a step
 
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 template <typename MT, int D>
 struct Tile {
+  typedef TileShape<D, sizeof(MT) == 2> S;
   static constexpr int ES = sizeof(MT), RC = D * ES / 16;  // 16-byte parts of a row
+  static constexpr int WAVES = S::WAVES, THREADS = 64 * WAVES, ROWS = S::ROWS;
   static constexpr int BYTES = SUB * D * ES;               // one step's keys (or values)
-  static constexpr int NL = BYTES / 16 / kThreads;         // 16-byte loads per thread of them
+  static constexpr int PARTS = BYTES / 16;
+  static constexpr int NL = (PARTS + THREADS - 1) / THREADS;  // 16-byte loads per thread of them
   static constexpr int SF = RC / 2;                        // operand fragments of a score
   static constexpr int NC = D / 32;                        // 32-channel tiles of the output
   // PIPE: scores of step i + 1 beside the softmax of i and the output of i - 1, with keys i .. i + 2 and
-  // values i - 1 .. i + 1 in LDS. fp32 heads of 256 channels have no room for that: keys and values of
-  // steps i and i + 1.
-  static constexpr bool PIPE = BYTES < 32768;
+  // values i - 1 .. i + 1 in LDS; otherwise keys and values of steps i and i + 1. In fp32 the products take
+  // 25 times as long as the softmax, so there is nothing to gain.
+  static constexpr bool PIPE = ES == 2;
   static constexpr int AHEAD = PIPE ? 2 : 1, KSLOTS = AHEAD + 1, VSLOTS = PIPE ? 3 : 2;
   static constexpr int LDS = (KSLOTS + VSLOTS) * BYTES;
 };
@@ -74,6 +76,7 @@ template <> struct Op<bf16> {
     return w;
   }
   static constexpr int NF = 2;  // fragments of a step's weights
+  __device__ __forceinline__ static void hold(weights& w) { asm volatile("" : "+v"(w.f[0]), "+v"(w.f[1])); }
   __device__ __forceinline__ static f32x16 value(bf16x8 v, const weights& w, int i, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w.f[i], c, 0, 0, 0);
   }
@@ -88,6 +91,7 @@ template <> struct Op<float> {
   }
   __device__ __forceinline__ static weights pack(const f32x16& s) { return {s}; }
   static constexpr int NF = 16;
+  __device__ __forceinline__ static void hold(weights& w) { asm volatile("" : "+v"(w.f)); }
   __device__ __forceinline__ static f32x16 value(float v, const weights& w, int i, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x2f32(v, w.f[i], c, 0, 0, 0);
   }
@@ -109,18 +113,15 @@ __device__ __forceinline__ float value_frag(const char* v, int lane, int i, int 
 }
 
 // O^T += V^T P^T
-template <typename MT, int D, int NQ>
-__device__ __forceinline__ void add_values(const char* v, int lane, const typename Op<MT>::weights (&p)[NQ],
-                                           f32x16 (&acc)[NQ][D / 32]) {
+template <typename MT, int D>
+__device__ __forceinline__ void add_values(const char* v, int lane, const typename Op<MT>::weights& p,
+                                           f32x16 (&acc)[D / 32]) {
 #pragma unroll
   for (int i = 0; i < Op<MT>::NF; ++i)
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const auto f = value_frag<D>(v, lane, i, c, MT());
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) acc[q][c] = Op<MT>::value(f, p[q], i, acc[q][c]);
-    }
+    for (int c = 0; c < D / 32; ++c) acc[c] = Op<MT>::value(value_frag<D>(v, lane, i, c, MT()), p, i, acc[c]);
 }
+
 // ------------------------------------------------------------------ the plan
 constexpr int kPlan = 1024;
 __global__ __launch_bounds__(kPlan) void tile_plan_kernel(AttnArgs a) {
@@ -182,100 +183,116 @@ __global__ __launch_bounds__(kPlan) void tile_plan_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------------ the kernel
-template <typename MT, int D, int NQ>
-__global__ __launch_bounds__(kThreads, 1) void tile_kernel(AttnArgs a) {
+// Where a workgroup is in its share: kept in LDS between tiles, and the arguments read again
+// where they are needed, so that the steps' loop holds no scalar registers that it does not use.
+struct Walk {
+  int64_t at, end, begin, t0, nt;  // units; the sequence's tiles t0 .. t0 + nt - 1
+  int n, h, tile, off;             // off: units of the tile that are done
+};
+__device__ __forceinline__ AttnArgs fresh_args() {
+  auto p = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnArgs*)(const void*)p;
+}
+
+template <typename MT, int D>
+__global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD)) void tile_kernel(AttnArgs) {
   typedef Tile<MT, D> T;
   typedef typename Op<MT>::weights weights;
-  constexpr int RC = T::RC, NL = T::NL, SF = T::SF, NC = T::NC, ROWS = 128 * NQ;
+  constexpr int kThreads = T::THREADS, kWaves = T::WAVES, kGroups = T::S::GROUPS, ROWS = T::ROWS;
+  constexpr int RC = T::RC, NL = T::NL, SF = T::SF, NC = T::NC, ES = T::ES, BYTES = T::BYTES;
   constexpr int KSLOTS = T::KSLOTS, VSLOTS = T::VSLOTS, AHEAD = T::AHEAD;
   __shared__ __align__(16) char lds[T::LDS];
   __shared__ int odd_at[VSLOTS][kWaves], counts[kWaves];
+  __shared__ Walk walk;
   char* const kl = lds;
-  char* const vl = lds + KSLOTS * T::BYTES;
+  char* const vl = lds + KSLOTS * BYTES;
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, h2 = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int N = a.b.num_seqs, Hk = a.num_kv_heads, G = a.num_q_heads / Hk, ps = a.b.page_size,
-            shift = __builtin_ctz(ps);
-  const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, ROWS));
+  const int share = (blockIdx.x % 8) * (kGroups / 8) + blockIdx.x / 8;
 
   // --- this workgroup's share of all units. The shares of the workgroups of one XCD (every
   // eighth) lie side by side, so that they read the same heads' keys through one L2.
-  const int64_t total = Hk * pl.pre[pl.tile_first[N]], per = max((int64_t)1, (total + kTileGroups - 1) / kTileGroups);
-  const int share = (blockIdx.x % 8) * (kTileGroups / 8) + blockIdx.x / 8;
-  int64_t at = share * per;
-  const int64_t begin = at, end = min(total, at + per);
-  if (at >= end) return;
-  // the entries of a sorted array that are at most x, counted over the threads
-  auto count = [&](const int64_t* v, int64_t n, auto value, int64_t x) {
-    int c = 0;
-    for (int64_t i = tid; i < n; i += kThreads) c += value(v[i]) <= x;
+  {
+    const AttnArgs a = fresh_args();
+    const int N = a.b.num_seqs, Hk = a.num_kv_heads, G = a.num_q_heads / Hk;
+    const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, ROWS));
+    const int64_t total = Hk * pl.pre[pl.tile_first[N]], per = max((int64_t)1, (total + kGroups - 1) / kGroups);
+    const int64_t at = share * per;
+    if (at >= total) return;
+    // the entries of a sorted array that are at most x, counted over the threads
+    auto count = [&](int64_t n, auto entry, int64_t x) {
+      int c = 0;
+      for (int64_t i = tid; i < n; i += kThreads) c += entry(i) <= x;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d);
-    __syncthreads();
-    if (lane == 0) counts[wave] = c;
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(counts[0] + counts[1] + counts[2] + counts[3]);
-  };
-  int n = count(pl.tile_first + 1, N, [&](int64_t f) { return Hk * pl.pre[f]; }, at);
-  int64_t t0 = pl.tile_first[n], nt = pl.tile_first[n + 1] - t0;
-  int64_t per_head = pl.pre[t0 + nt] - pl.pre[t0];
-  int h = (int)((at - Hk * pl.pre[t0]) / per_head);
-  int64_t off = at - Hk * pl.pre[t0] - h * per_head;  // unit within the (sequence, head)
-  int tile = count(pl.pre + t0 + 1, nt, [&](int64_t f) { return f - pl.pre[t0]; }, off);
-  off -= pl.pre[t0 + tile] - pl.pre[t0];              // unit within the tile
-
-  const float c = a.scale * LOG2E, slack = 8.f / c;
-  while (at < end) {
-    if (tile == nt) {
-      tile = 0;
-      if (++h == Hk) {
-        h = 0;
-        do ++n, t0 += nt, nt = pl.tile_first[n + 1] - t0;
-        while (nt == 0);
+      for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d);
+      __syncthreads();
+      if (lane == 0) counts[wave] = c;
+      __syncthreads();
+      int all = 0;
+      for (int w = 0; w < kWaves; ++w) all += counts[w];
+      return all;
+    };
+    const int n = count(N, [&](int64_t i) { return Hk * pl.pre[pl.tile_first[i + 1]]; }, at);
+    const int64_t t0 = pl.tile_first[n], nt = pl.tile_first[n + 1] - t0, u0 = pl.pre[t0];
+    const int64_t per_head = pl.pre[t0 + nt] - u0;
+    const int h = (int)((at - Hk * u0) / per_head);
+    const int64_t off = at - Hk * u0 - h * per_head;
+    const int tile = count(nt, [&](int64_t i) { return pl.pre[t0 + i + 1] - u0; }, off);
+    if (tid == 0) walk = {at, min(total, at + per), at, t0, nt, n, h, tile, (int)(off - (pl.pre[t0 + tile] - u0))};
+  }
+  for (;;) {
+    __syncthreads();  // `walk` is up to date, and LDS free of the last tile's use
+    if (walk.at >= walk.end) return;
+    if (walk.tile == walk.nt) {
+      __syncthreads();
+      if (tid == 0) {
+        const AttnArgs a = fresh_args();
+        const int G = a.num_q_heads / a.num_kv_heads;
+        const TilePlan pl = tile_plan_at(a.tile_ws, a.b.num_seqs, max_tiles(a.b.num_seqs, a.b.total_tokens, G, ROWS));
+        walk.tile = 0;
+        if (++walk.h == a.num_kv_heads) {
+          walk.h = 0;
+          do ++walk.n, walk.t0 += walk.nt, walk.nt = pl.tile_first[walk.n + 1] - walk.t0;
+          while (walk.nt == 0);
+        }
       }
-      off = 0;
+      continue;
     }
+    const AttnArgs a = fresh_args();
+    const int n = __builtin_amdgcn_readfirstlane(walk.n), h = __builtin_amdgcn_readfirstlane(walk.h),
+              tile = __builtin_amdgcn_readfirstlane(walk.tile), off = __builtin_amdgcn_readfirstlane(walk.off);
+    const int left = __builtin_amdgcn_readfirstlane((int)min(walk.end - walk.at, (int64_t)INT32_MAX));
+    const int G = a.num_q_heads / a.num_kv_heads, ps1 = a.b.page_size - 1, shift = __builtin_ctz(a.b.page_size);
     const Seq s = seq_at(a, n, G, SUB);
     const TileKeys tk = tile_keys(a, s, tile, G);
-    const int u0 = (int)off, u1 = (int)min((int64_t)tk.units, u0 + (end - at));
-    if (tk.units == 0) {
-      ++tile;
-      off = 0;
+    const int nb = min(tk.units - off, left);  // steps
+    if (nb <= 0) {                             // a tile without keys
+      __syncthreads();
+      if (tid == 0) ++walk.tile, walk.off = 0;
       continue;
     }
 
-    // --- the wave's rows: lane m's queries and their visible keys; the ranges that some row
-    // (any) and every row (full) sees, of the wave and of the workgroup
-    int plo[NQ], phi[NQ];
-    v4u32 qf[NQ][SF];
-    int any_lo = INT32_MAX, any_hi = -1, full_lo = 0, full_hi = INT32_MAX;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int row = tile * ROWS + (wave * NQ + q) * 32 + m;
-      const bool has = row < s.rows;
+    // --- the wave's rows: lane m's query and its visible keys plo .. phi; the ranges that every row of the
+    // wave sees (full), and that some (any) and every row of the workgroup sees
+    const int row = tile * ROWS + wave * 32 + m;
+    const bool has = row < s.rows;
+    int plo, phi;
+    v4u32 qf[SF];
+    {
       const int tok = has ? row / G : 0, hq = h * G + (has ? row - tok * G : 0), p = s.p0 + tok;
-      phi[q] = has ? min(p, s.hi - 1) : -1;
-      plo[q] = a.window ? max(0, p - a.window + 1) : 0;
-      const MT* src = (const MT*)a.q + (s.row0 + tok) * a.q_stride + hq * D;
+      phi = has ? min(p, s.hi - 1) : -1;
+      plo = a.window ? max(0, p - a.window + 1) : 0;
+      const char* src = (const char*)((const MT*)a.q + (s.row0 + tok) * a.q_stride + hq * D) + h2 * 16;
 #pragma unroll
-      for (int i = 0; i < SF; ++i) {
-        qf[q][i] = *reinterpret_cast<const v4u32*>((const char*)src + (2 * i + h2) * 16);
-        if (!has) qf[q][i] = v4u32{0, 0, 0, 0};
-      }
-      any_lo = min(any_lo, has ? plo[q] : INT32_MAX);
-      any_hi = max(any_hi, phi[q]);
-      full_lo = max(full_lo, has ? plo[q] : 0);
-      full_hi = min(full_hi, has ? phi[q] : INT32_MAX);
+      for (int i = 0; i < SF; ++i) qf[i] = *reinterpret_cast<const v4u32*>(src + 32 * i);
     }
+    int full_lo = has ? plo : 0, full_hi = has ? phi : INT32_MAX;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      any_lo = min(any_lo, __shfl_xor(any_lo, d));
-      any_hi = max(any_hi, __shfl_xor(any_hi, d));
       full_lo = max(full_lo, __shfl_xor(full_lo, d));
       full_hi = min(full_hi, __shfl_xor(full_hi, d));
     }
-    any_lo = __builtin_amdgcn_readfirstlane(any_lo);
-    any_hi = __builtin_amdgcn_readfirstlane(any_hi);
     full_lo = __builtin_amdgcn_readfirstlane(full_lo);
     full_hi = __builtin_amdgcn_readfirstlane(full_hi);
     // rows of the tile run over consecutive tokens, so its ranges follow from the first and last
@@ -285,49 +302,61 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(AttnArgs a) {
     const int w_any_lo = a.window ? max(0, pf - a.window + 1) : 0, w_full_lo = a.window ? max(0, pe - a.window + 1) : 0;
 
     const int32_t* table = a.b.block_table + n * a.b.table_stride;
-    const int64_t head = (int64_t)h * ps * D;
-    const int key0 = tk.lo + u0 * SUB, nb = u1 - u0;
+    const int num_pages = a.b.num_pages;
+    const int key0 = tk.lo + off * SUB, hi_key = min(s.hi, key0 + nb * SUB);
+    const int64_t kstride = a.k_page_stride * ES, vstride = a.v_page_stride * ES;
+    const char* const kbase = a.k_pages + (int64_t)h * (ps1 + 1) * D * ES;
+    const char* const vbase = a.v_pages + (int64_t)h * (ps1 + 1) * D * ES;
+    const float c = a.scale * LOG2E, slack = 8.f / c;
 
-    // --- staging: step i's keys and values, thread by thread in 16-byte parts
-    auto entries = [&](int i, int (&e)[2]) __attribute__((always_inline)) {
+    // --- staging: a step's keys and values, thread by thread in 16-byte parts.
+    // Step i's table entries are read a step before they are needed (raw), so that nothing waits for them.
+    auto read_entries = [&](int i, int (&raw)[2]) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int key = key0 + i * SUB + 16 * t;
-        int x = -1;
-        if (i < nb && key < s.hi) x = table[key >> shift];
-        x = __builtin_amdgcn_readfirstlane(x);
-        e[t] = page_ok(x, a.b.num_pages) ? x : -1;
+        raw[t] = key < hi_key ? table[key >> shift] : -1;
       }
     };
-    auto fetch = [&](const char* pages, int64_t stride, int i, const int (&e)[2], v4u32 (&r)[NL]) __attribute__((always_inline)) {
+    auto check_entries = [&](const int (&raw)[2], int (&e)[2]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        const int grp = (j * kThreads + wave * 64) / RC / 16;  // 16-key group of the wave's rows
-        const int key = key0 + i * SUB + 16 * grp;
-        const MT* src = (const MT*)pages + max(grp ? e[1] : e[0], 0) * stride + head + (key & (ps - 1)) * D;
-        r[j] = *reinterpret_cast<const v4u32*>((const char*)src + (j * kThreads + tid - grp * 16 * RC) * 16);
+      for (int t = 0; t < 2; ++t) {
+        const int x = __builtin_amdgcn_readfirstlane(raw[t]);
+        e[t] = page_ok(x, num_pages) ? x : -1;
       }
     };
-    auto put_k = [&](int i, const v4u32 (&r)[NL]) __attribute__((always_inline)) {
+    auto fetch = [&](const char* base, int64_t stride, int i, const int (&e)[2], v4u32 (&r)[NL]) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
+        if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
+        const int part = j * kThreads + wave * 64, grp = part / RC / 16;  // the 16-key group of the wave's rows
+        const char* src = base + max(grp ? e[1] : e[0], 0) * stride + ((key0 + i * SUB + 16 * grp) & ps1) * (D * ES) +
+                          (part - grp * 16 * RC) * 16;
+        r[j] = *reinterpret_cast<const v4u32*>(src + (unsigned)lane * 16u);
+      }
+    };
+    auto put_k = [&](int slot, const v4u32 (&r)[NL]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < NL; ++j) {
+        if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
         const int x = j * kThreads + tid;
-        *reinterpret_cast<v4u32*>(kl + (i % KSLOTS) * T::BYTES + k_at<MT, D>(x / RC, x % RC)) = r[j];
+        *reinterpret_cast<v4u32*>(kl + slot + k_at<MT, D>(x / RC, x % RC)) = r[j];
       }
     };
-    // whether a step is seen whole by every row of the range, and none of its pages is missing
+    // whether a step's keys are all in the range, and none of its pages is missing
     auto whole = [&](int i, const int (&e)[2], int lo, int hi) __attribute__((always_inline)) {
       const int kb = key0 + i * SUB;
-      return kb >= lo && kb + SUB - 1 <= hi && e[0] >= 0 && e[1] >= 0;
+      return kb >= lo && kb + SUB - 1 <= hi && (e[0] | e[1]) >= 0;
     };
     // Values that no row sees become 0. So does an infinity or NaN where some row does not see it, since a
     // weight of 0 would not hide it; the step is then marked, and the rows that do see it get it
-    // from `add`.
-    auto put_v = [&](int i, const int (&e)[2], v4u32 (&r)[NL]) __attribute__((always_inline)) {
+    // from add_odd.
+    auto put_v = [&](int i, int slot, const int (&e)[2], v4u32 (&r)[NL]) __attribute__((always_inline)) {
       if (!whole(i, e, w_full_lo, w_full_hi)) {
         bool odd = false;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
+          if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
           const int x = (j * kThreads + tid) / RC, key = key0 + i * SUB + x;
           if (key < w_any_lo || key > w_any_hi || (x < 16 ? e[0] : e[1]) < 0) r[j] = v4u32{0, 0, 0, 0};
           odd |= any_nonfinite<MT>(r[j]);
@@ -338,70 +367,58 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
+        if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
         const int x = j * kThreads + tid;
-        *reinterpret_cast<v4u32*>(vl + (i % VSLOTS) * T::BYTES + v_at<MT, D>(x / RC, x % RC)) = r[j];
-      }
-    };
-    auto scores = [&](int i, f32x16 (&st)[NQ]) __attribute__((always_inline)) {
-      const char* k = kl + (i % KSLOTS) * T::BYTES;
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) st[q] = f32x16{};
-#pragma unroll
-      for (int f = 0; f < SF; ++f) {
-        const v4u32 kf = *reinterpret_cast<const v4u32*>(k + k_at<MT, D>(m, 2 * f + h2));
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) st[q] = Op<MT>::score(kf, qf[q][f], st[q]);
+        *reinterpret_cast<v4u32*>(vl + slot + v_at<MT, D>(x / RC, x % RC)) = r[j];
       }
     };
 
-    f32x16 acc[NQ][NC] = {};
-    float mx[NQ], sum[NQ];
+    f32x16 acc[NC] = {};
+    float mx = -INFINITY, sum = 0.f;
+    auto scores = [&](int slot, f32x16& st) __attribute__((always_inline)) {
+      st = f32x16{};
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) mx[q] = -INFINITY, sum[q] = 0.f;
-
-    auto mask = [&](int i, const int (&e)[2], f32x16 (&st)[NQ]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = key0 + i * SUB + 8 * (r / 4) + 4 * h2 + r % 4;
-          if (key < plo[q] || key > phi[q] || e[r / 8] < 0) st[q][r] = -INFINITY;
-        }
+      for (int f = 0; f < SF; ++f)
+        st = Op<MT>::score(*reinterpret_cast<const v4u32*>(kl + slot + k_at<MT, D>(m, 2 * f + h2)), qf[f], st);
     };
-    // softmax of one step: weights, running maximum and sum, and the factors for the output
-    auto softmax = [&](f32x16 (&st)[NQ], weights (&p)[NQ], float (&al)[NQ]) __attribute__((always_inline)) {
+    auto mask = [&](int i, const int (&e)[2], f32x16& st) __attribute__((always_inline)) {
+      const int kb = key0 + i * SUB + 4 * h2;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        float tm = st[q][0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) tm = fmaxf(tm, st[q][r]);
-        tm = across32(tm, MaxOp());
-        const float mn = tm > mx[q] + slack ? tm : mx[q], mu = mn == -INFINITY ? 0.f : mn, mc = mu * c;
-        al[q] = exp2_f(mx[q] * c - mc);
-        mx[q] = mn;
-        float t = 0.f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          st[q][r] = exp2_f(fmaf(st[q][r], c, -mc));
-          t += st[q][r];
-        }
-        sum[q] = sum[q] * al[q] + t;
-        p[q] = Op<MT>::pack(st[q]);
+      for (int r = 0; r < 16; ++r) {
+        const int key = kb + 8 * (r / 4) + r % 4;
+        if ((key < plo) | (key > phi) | (e[r / 8] < 0)) st[r] = -INFINITY;
       }
     };
-    auto rescale = [&](const float (&al)[NQ]) __attribute__((always_inline)) {
-      bool any = false;
+    // softmax of one step: weights, running maximum and sum, and the factor for the output
+    auto softmax = [&](f32x16& st, weights& p, float& al) __attribute__((always_inline)) {
+      float tm = max3(st[0], st[1], st[2]);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) any |= al[q] != 1.f;
-      if (__any(any)) {
+      for (int r = 3; r < 15; r += 2) tm = max3(tm, st[r], st[r + 1]);
+      tm = max3(tm, st[15], st[15]);
+      tm = across32_max(tm);
+      const bool up = tm > mx + slack;
+      const float mn = up ? tm : mx, mc = mn == -INFINITY ? 0.f : mn * c;
+      al = up ? exp2_f(fmaf(mx, c, -mc)) : 1.f;
+      mx = mn;
+      float t[4];
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
+      for (int r = 0; r < 16; ++r) {
+        st[r] = exp2_f(fmaf(st[r], c, -mc));
+        t[r % 4] = r < 4 ? st[r] : t[r % 4] + st[r];
+      }
+      sum = fmaf(sum, al, (t[0] + t[1]) + (t[2] + t[3]));
+      p = Op<MT>::pack(st);
+      // (held here, or they would be sunk to where they are used, a step later)
+      Op<MT>::hold(p);
+      asm volatile("" : "+v"(sum));
+    };
+    auto rescale = [&](float al) __attribute__((always_inline)) {
+      if (__any(al != 1.f)) {
 #pragma unroll
-          for (int x = 0; x < NC; ++x) acc[q][x] *= al[q];
+        for (int x = 0; x < NC; ++x) acc[x] *= al;
       }
     };
-    auto add = [&](int i, const int (&e)[2], const weights (&p)[NQ]) __attribute__((always_inline)) {
-      add_values<MT, D, NQ>(vl + ((i + VSLOTS) % VSLOTS) * T::BYTES, lane, p, acc);
+    auto add_odd = [&](int i, const int (&e)[2]) __attribute__((always_inline)) {
       if (i >= 0 && !whole(i, e, w_full_lo, w_full_hi)) {
         bool odd = false;
 #pragma unroll
@@ -411,14 +428,11 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(AttnArgs a) {
           for (int x = 0; x < SUB; ++x) {
             const int key = key0 + i * SUB + x, pg = x < 16 ? e[0] : e[1];
             if (key > w_any_hi || pg < 0) continue;
-            const MT* v = (const MT*)a.v_pages + pg * a.v_page_stride + head + (key & (ps - 1)) * D;
+            const MT* v = (const MT*)(vbase + pg * vstride) + (key & ps1) * D;
 #pragma unroll
             for (int y = 0; y < NC * 16; ++y) {
               const float f = (float)v[32 * (y / 16) + 8 * (y / 4 % 4) + 4 * h2 + y % 4];
-              if (f - f != 0.f)
-#pragma unroll
-                for (int q = 0; q < NQ; ++q)
-                  if (key >= plo[q] && key <= phi[q]) acc[q][y / 16][y % 16] += f;
+              if (f - f != 0.f && key >= plo && key <= phi) acc[y / 16][y % 16] += f;
             }
           }
         }
@@ -426,99 +440,122 @@ __global__ __launch_bounds__(kThreads, 1) void tile_kernel(AttnArgs a) {
     };
 
     // --- the steps. During step i the keys of i + AHEAD and the values of i + 1 are fetched, and put
-    // in LDS at its end.
+    // in LDS at its end. (Behind the last step the fetches read page 0, and the scores are of what lies in
+    // LDS: nobody reads either.)
     v4u32 kr[NL], vr[NL];
-    int ep[2] = {-1, -1}, e0[2], e1[2], e2[2], e3[2];  // pages of steps i - 1 .. i + 3
-    entries(0, e0);
-    entries(1, e1);
-    entries(2, e2);
-    __syncthreads();  // LDS is free of the last tile's use
-    fetch(a.k_pages, a.k_page_stride, 0, e0, kr);
-    fetch(a.v_pages, a.v_page_stride, 0, e0, vr);
+    int ep[2] = {-1, -1}, e0[2], e1[2], e2[2], raw[2];  // pages of steps i - 1 .. i + 2, entries of i + 2
+    read_entries(0, raw);
+    check_entries(raw, e0);
+    read_entries(1, raw);
+    check_entries(raw, e1);
+    read_entries(2, raw);
+    fetch(kbase, kstride, 0, e0, kr);
+    fetch(vbase, vstride, 0, e0, vr);
     put_k(0, kr);
-    put_v(0, e0, vr);
+    put_v(0, 0, e0, vr);
     if (T::PIPE) {
       // "step -1", whose weights are 0
+      for (int x = tid; x < T::PARTS; x += kThreads)
+        *reinterpret_cast<v4u32*>(vl + (VSLOTS - 1) * BYTES + x * 16) = v4u32{0, 0, 0, 0};
+      fetch(kbase, kstride, 1, e1, kr);
+      put_k(BYTES, kr);
+    }
+    __syncthreads();
+    weights pa = {}, pb;
+    f32x16 sa, sb;
+    // slots: of the next step's scores or (not PIPE) this one's, of what is put, of the values
+    int kread = T::PIPE ? BYTES : 0, kput = AHEAD % KSLOTS * BYTES, vread = T::PIPE ? (VSLOTS - 1) * BYTES : 0, vput = BYTES;
+    auto next = [](int slot, int slots) { return slot == (slots - 1) * BYTES ? 0 : slot + BYTES; };
+    if (T::PIPE) scores(0, sa);
+    auto step = [&](int i, f32x16& cur, f32x16& nxt, weights& p, weights& pn) __attribute__((always_inline)) {
+      check_entries(raw, e2);
+      fetch(kbase, kstride, i + AHEAD, AHEAD == 2 ? e2 : e1, kr);
+      fetch(vbase, vstride, i + 1, e1, vr);
+      read_entries(i + 3, raw);
+      float al;
+      if (!T::PIPE) scores(kread, cur);
+      if (!whole(i, e0, full_lo, full_hi)) mask(i, e0, cur);
+      if (T::PIPE) {
+        scores(kread, nxt);
+        softmax(cur, pn, al);
+        add_values<MT, D>(vl + vread, lane, p, acc);
+        add_odd(i - 1, ep);
+        rescale(al);
+      } else {
+        softmax(cur, pn, al);
+        rescale(al);
+        add_values<MT, D>(vl + vread, lane, pn, acc);
+        add_odd(i, e0);
+      }
+      put_k(kput, kr);
+      put_v(i + 1, vput, e1, vr);
+      kread = next(kread, KSLOTS), kput = next(kput, KSLOTS), vread = next(vread, VSLOTS), vput = next(vput, VSLOTS);
 #pragma unroll
-      for (int j = 0; j < NL; ++j)
-        *reinterpret_cast<v4u32*>(vl + (VSLOTS - 1) * T::BYTES + (j * kThreads + tid) * 16) = v4u32{0, 0, 0, 0};
-      if (nb > 1) {
-        fetch(a.k_pages, a.k_page_stride, 1, e1, kr);
-        put_k(1, kr);
+      for (int t = 0; t < 2; ++t) ep[t] = e0[t], e0[t] = e1[t], e1[t] = e2[t];
+      lds_barrier();
+    };
+    if constexpr (T::PIPE) {
+      int i = 0;
+#pragma unroll 1
+      for (; i + 1 < nb; i += 2) {
+        step(i, sa, sb, pa, pb);
+        step(i + 1, sb, sa, pb, pa);
+      }
+      if (i < nb) {
+        step(i, sa, sb, pa, pb);
+        pa = pb;
+      }
+      add_values<MT, D>(vl + vread, lane, pa, acc);
+      add_odd(nb - 1, ep);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < nb; ++i) step(i, sa, sa, pa, pa);
+    }
+
+    // --- out
+    {
+      const AttnArgs a = fresh_args();
+      const int N = a.b.num_seqs, G = a.num_q_heads / a.num_kv_heads;
+      const int n = walk.n, h = walk.h, tile = walk.tile, off = walk.off;
+      const Seq s = seq_at(a, n, G, SUB);
+      const TileKeys tk = tile_keys(a, s, tile, G);
+      const bool done = off == 0 && nb == tk.units;
+      const int r = wave * 32 + m, row = tile * ROWS + r;
+      const float l = across32(sum, SumOp());
+      if (row < s.rows) {
+        if (done) {
+          const int tok = row / G;
+          const int64_t out = (s.row0 + tok) * a.num_q_heads + h * G + row - tok * G;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          MT* dst = (MT*)a.o + out * D + 4 * h2;
+#pragma unroll
+          for (int x = 0; x < NC; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dst[32 * x + 8 * y + e] = from_f32<MT>(acc[x][4 * y + e] * inv);
+          if (a.lse && h2 == 0) a.lse[out] = mx * a.scale + (l == 0.f ? 0.f : logf(l));
+        } else {
+          const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, ROWS));
+          float* part = pl.part + (2 * (int64_t)share + (walk.at == walk.begin ? 0 : 1)) * tile_part_floats(ROWS, D);
+#pragma unroll
+          for (int x = 0; x < NC; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<f32x4*>(part + (int64_t)r * D + 32 * x + 8 * y + 4 * h2) =
+                  f32x4{acc[x][4 * y], acc[x][4 * y + 1], acc[x][4 * y + 2], acc[x][4 * y + 3]};
+          if (h2 == 0) part[ROWS * D + 2 * r] = mx, part[ROWS * D + 2 * r + 1] = l;
+        }
       }
     }
     __syncthreads();
-    weights p[NQ] = {}, pn[NQ];
-    f32x16 cur[NQ], nxt[NQ];
-    float al[NQ];
-    if (T::PIPE) scores(0, cur);
-#pragma unroll 1
-    for (int i = 0; i < nb; ++i) {
-      if (i + AHEAD < nb) fetch(a.k_pages, a.k_page_stride, i + AHEAD, AHEAD == 2 ? e2 : e1, kr);
-      if (i + 1 < nb) fetch(a.v_pages, a.v_page_stride, i + 1, e1, vr);
-      entries(i + 3, e3);
-      // (behind the last step, the scores of what lies in LDS, which nobody reads)
-      scores(T::PIPE ? i + 1 : i, T::PIPE ? nxt : cur);
-      if (!whole(i, e0, full_lo, full_hi)) mask(i, e0, cur);
-      softmax(cur, pn, al);
-      if (T::PIPE) add(i - 1, ep, p);
-      rescale(al);
-      if (!T::PIPE) add(i, e0, pn);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        p[q] = pn[q];
-        if (T::PIPE) cur[q] = nxt[q];
-      }
-      if (i + AHEAD < nb) put_k(i + AHEAD, kr);
-      if (i + 1 < nb) put_v(i + 1, e1, vr);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) ep[t] = e0[t], e0[t] = e1[t], e1[t] = e2[t], e2[t] = e3[t];
-      lds_barrier();
-    }
-    if (T::PIPE) add(nb - 1, ep, p);
-
-    // --- out
-    const bool done = u0 == 0 && u1 == tk.units;
-    float* part = pl.part + (2 * (int64_t)share + (at == begin ? 0 : 1)) * tile_part_floats(ROWS, D);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int r = (wave * NQ + q) * 32 + m, row = tile * ROWS + r;
-      const float l = across32(sum[q], SumOp());
-      if (row >= s.rows) continue;
-      if (done) {
-        const int tok = row / G;
-        const int64_t out = (s.row0 + tok) * a.num_q_heads + h * G + row - tok * G;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        MT* dst = (MT*)a.o + out * D + 4 * h2;
-#pragma unroll
-        for (int x = 0; x < NC; ++x)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[32 * x + 8 * y + e] = from_f32<MT>(acc[q][x][4 * y + e] * inv);
-        if (a.lse && h2 == 0) a.lse[out] = mx[q] * a.scale + (l == 0.f ? 0.f : logf(l));
-      } else {
-#pragma unroll
-        for (int x = 0; x < NC; ++x)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<f32x4*>(part + (int64_t)r * D + 32 * x + 8 * y + 4 * h2) =
-                f32x4{acc[q][x][4 * y], acc[q][x][4 * y + 1], acc[q][x][4 * y + 2], acc[q][x][4 * y + 3]};
-        if (h2 == 0) part[ROWS * D + 2 * r] = mx[q], part[ROWS * D + 2 * r + 1] = l;
-      }
-    }
-    at += u1 - u0;
-    off = 0;
-    ++tile;
+    if (tid == 0) walk.at += nb, ++walk.tile, walk.off = 0;
   }
 }
 
 template <typename MT, int D>
 void launch(const AttnArgs& a) {
-  if constexpr (attn_tile_rows(D, sizeof(MT) == 2) == 256)
-    tile_kernel<MT, D, 2><<<kTileGroups, kThreads, 0, a.stream>>>(a);
-  else
-    tile_kernel<MT, D, 1><<<kTileGroups, kThreads, 0, a.stream>>>(a);
+  tile_kernel<MT, D><<<Tile<MT, D>::S::GROUPS, Tile<MT, D>::THREADS, 0, a.stream>>>(a);
 }
 
 }  // namespace
@@ -536,9 +573,10 @@ void launch_attn_tile(const AttnArgs& a) {
   }
 }
 
-size_t attn_tile_bytes(int num_seqs, int64_t total_tokens, int G, int head_dim, int tile_rows) {
-  return tile_plan_bytes(num_seqs, max_tiles(num_seqs, total_tokens, G, tile_rows)) +
-         (size_t)(2 * kTileGroups * tile_part_floats(tile_rows, head_dim)) * 4;
+size_t attn_tile_bytes(int num_seqs, int64_t total_tokens, int G, int head_dim, bool bf16) {
+  const int rows = attn_tile_rows(head_dim, bf16), groups = attn_tile_groups(head_dim, bf16);
+  return tile_plan_bytes(num_seqs, max_tiles(num_seqs, total_tokens, G, rows)) +
+         (size_t)(2 * groups * tile_part_floats(rows, head_dim)) * 4;
 }
 
 }  // namespace kda
