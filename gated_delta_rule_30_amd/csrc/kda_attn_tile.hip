@@ -309,29 +309,59 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const char* const vbase = a.v_pages + (int64_t)h * (ps1 + 1) * D * ES;
     const float c = a.scale * LOG2E, slack = 8.f / c;
 
-    // --- staging: a step's keys and values, thread by thread in 16-byte parts.
-    // Step i's table entries are read a step before they are needed (raw), so that nothing waits for them.
-    auto read_entries = [&](int i, int (&raw)[2]) __attribute__((always_inline)) {
+    // --- staging: a step's keys and values, thread by thread in 16-byte parts. A wave's parts lie in
+    // one 16-key group of the step, or (GRPS 2) half of them in each; a group lies in one page.
+    // The table is read for 64 steps at once, a step per lane, 64 steps ahead: where a step's
+    // keys and values start is a lane of kat, vat, and whether its pages exist a bit of `pages`.
+    constexpr int GRPS = NL > 1 ? 2 : 1;
+    const int grp0 = GRPS == 2 ? 0 : wave * 64 / RC / 16;
+    int64_t kat[GRPS], vat[GRPS];
+    uint64_t pages[2];
+    int ahead[2];
+    auto read_table = [&](int block) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int key = key0 + i * SUB + 16 * t;
-        raw[t] = key < hi_key ? table[key >> shift] : -1;
+        const int key = key0 + (block * 64 + lane) * SUB + 16 * t;
+        ahead[t] = key < hi_key ? table[key >> shift] : -1;
       }
     };
-    auto check_entries = [&](const int (&raw)[2], int (&e)[2]) __attribute__((always_inline)) {
+    auto take_table = [&](int block) __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int x = __builtin_amdgcn_readfirstlane(raw[t]);
-        e[t] = page_ok(x, num_pages) ? x : -1;
+      for (int t = 0; t < 2; ++t) pages[t] = __ballot(page_ok(ahead[t], num_pages));
+#pragma unroll
+      for (int g = 0; g < GRPS; ++g) {
+        const int t = GRPS == 2 ? g : grp0, key = key0 + (block * 64 + lane) * SUB + 16 * t;
+        const int x = t ? ahead[1] : ahead[0];
+        const int64_t page = page_ok(x, num_pages) ? x : 0, in = (key & ps1) * (D * ES);
+        kat[g] = page * kstride + in;
+        vat[g] = page * vstride + in;
       }
     };
-    auto fetch = [&](const char* base, int64_t stride, int i, const int (&e)[2], v4u32 (&r)[NL]) __attribute__((always_inline)) {
+    auto lane64 = [&](int64_t x, int l) __attribute__((always_inline)) {
+      const unsigned lo = __builtin_amdgcn_readlane((unsigned)x, l), hi = __builtin_amdgcn_readlane((unsigned)(x >> 32), l);
+      return (int64_t)((uint64_t)hi << 32 | lo);
+    };
+    struct Step {
+      int64_t k[GRPS], v[GRPS];
+      int ok;  // bit t: the page of group t exists
+    };
+    // where step i lies (called for i = 0, 1, 2, ..)
+    auto look_up = [&](int i, Step& x) __attribute__((always_inline)) {
+      const int l = i & 63;
+      if (l == 0) {
+        take_table(i >> 6);
+        read_table((i >> 6) + 1);
+      }
+#pragma unroll
+      for (int g = 0; g < GRPS; ++g) x.k[g] = lane64(kat[g], l), x.v[g] = lane64(vat[g], l);
+      x.ok = (int)(pages[0] >> l & 1) | (int)(pages[1] >> l & 1) << 1;
+    };
+    auto fetch = [&](const char* base, const int64_t (&at)[GRPS], v4u32 (&r)[NL]) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
         if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
-        const int part = j * kThreads + wave * 64, grp = part / RC / 16;  // the 16-key group of the wave's rows
-        const char* src = base + max(grp ? e[1] : e[0], 0) * stride + ((key0 + i * SUB + 16 * grp) & ps1) * (D * ES) +
-                          (part - grp * 16 * RC) * 16;
+        const int part = j * kThreads + wave * 64, g = GRPS == 2 ? part / RC / 16 : 0;  // (j alone decides it)
+        const char* src = base + (GRPS == 2 && g ? at[GRPS - 1] : at[0]) + (part - (GRPS == 2 ? g : grp0) * 16 * RC) * 16;
         r[j] = *reinterpret_cast<const v4u32*>(src + (unsigned)lane * 16u);
       }
     };
@@ -344,21 +374,21 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       }
     };
     // whether a step's keys are all in the range, and none of its pages is missing
-    auto whole = [&](int i, const int (&e)[2], int lo, int hi) __attribute__((always_inline)) {
+    auto whole = [&](int i, int ok, int lo, int hi) __attribute__((always_inline)) {
       const int kb = key0 + i * SUB;
-      return kb >= lo && kb + SUB - 1 <= hi && (e[0] | e[1]) >= 0;
+      return kb >= lo && kb + SUB - 1 <= hi && ok == 3;
     };
     // Values that no row sees become 0. So does an infinity or NaN where some row does not see it, since a
     // weight of 0 would not hide it; the step is then marked, and the rows that do see it get it
     // from add_odd.
-    auto put_v = [&](int i, int slot, const int (&e)[2], v4u32 (&r)[NL]) __attribute__((always_inline)) {
-      if (!whole(i, e, w_full_lo, w_full_hi)) {
+    auto put_v = [&](int i, int slot, int ok, v4u32 (&r)[NL]) __attribute__((always_inline)) {
+      if (!whole(i, ok, w_full_lo, w_full_hi)) {
         bool odd = false;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
           if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
           const int x = (j * kThreads + tid) / RC, key = key0 + i * SUB + x;
-          if (key < w_any_lo || key > w_any_hi || (x < 16 ? e[0] : e[1]) < 0) r[j] = v4u32{0, 0, 0, 0};
+          if (key < w_any_lo || key > w_any_hi || !(ok >> (x / 16) & 1)) r[j] = v4u32{0, 0, 0, 0};
           odd |= any_nonfinite<MT>(r[j]);
           r[j] = finite_part<MT>(r[j]);
         }
@@ -381,12 +411,12 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       for (int f = 0; f < SF; ++f)
         st = Op<MT>::score(*reinterpret_cast<const v4u32*>(kl + slot + k_at<MT, D>(m, 2 * f + h2)), qf[f], st);
     };
-    auto mask = [&](int i, const int (&e)[2], f32x16& st) __attribute__((always_inline)) {
+    auto mask = [&](int i, int ok, f32x16& st) __attribute__((always_inline)) {
       const int kb = key0 + i * SUB + 4 * h2;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int key = kb + 8 * (r / 4) + r % 4;
-        if ((key < plo) | (key > phi) | (e[r / 8] < 0)) st[r] = -INFINITY;
+        if ((key < plo) | (key > phi) | !(ok >> (r / 8) & 1)) st[r] = -INFINITY;
       }
     };
     // softmax of one step: weights, running maximum and sum, and the factor for the output
@@ -418,17 +448,17 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         for (int x = 0; x < NC; ++x) acc[x] *= al;
       }
     };
-    auto add_odd = [&](int i, const int (&e)[2]) __attribute__((always_inline)) {
-      if (i >= 0 && !whole(i, e, w_full_lo, w_full_hi)) {
+    auto add_odd = [&](int i, int ok) __attribute__((always_inline)) {
+      if (i >= 0 && !whole(i, ok, w_full_lo, w_full_hi)) {
         bool odd = false;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) odd |= odd_at[i % VSLOTS][w] != 0;
         if (__any(odd)) {
 #pragma unroll 1
           for (int x = 0; x < SUB; ++x) {
-            const int key = key0 + i * SUB + x, pg = x < 16 ? e[0] : e[1];
-            if (key > w_any_hi || pg < 0) continue;
-            const MT* v = (const MT*)(vbase + pg * vstride) + (key & ps1) * D;
+            const int key = key0 + i * SUB + x;
+            if (key > w_any_hi || !(ok >> (x / 16) & 1)) continue;
+            const MT* v = (const MT*)(vbase + table[key >> shift] * vstride) + (key & ps1) * D;
 #pragma unroll
             for (int y = 0; y < NC * 16; ++y) {
               const float f = (float)v[32 * (y / 16) + 8 * (y / 4 % 4) + 4 * h2 + y % 4];
@@ -443,21 +473,20 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     // in LDS at its end. (Behind the last step the fetches read page 0, and the scores are of what lies in
     // LDS: nobody reads either.)
     v4u32 kr[NL], vr[NL];
-    int ep[2] = {-1, -1}, e0[2], e1[2], e2[2], raw[2];  // pages of steps i - 1 .. i + 2, entries of i + 2
-    read_entries(0, raw);
-    check_entries(raw, e0);
-    read_entries(1, raw);
-    check_entries(raw, e1);
-    read_entries(2, raw);
-    fetch(kbase, kstride, 0, e0, kr);
-    fetch(vbase, vstride, 0, e0, vr);
+    Step x0, x1, x2;   // steps i, i + 1, i + 2
+    int okp = 0;       // x.ok of step i - 1
+    read_table(0);
+    look_up(0, x0);
+    look_up(1, x1);
+    fetch(kbase, x0.k, kr);
+    fetch(vbase, x0.v, vr);
     put_k(0, kr);
-    put_v(0, 0, e0, vr);
+    put_v(0, 0, x0.ok, vr);
     if (T::PIPE) {
       // "step -1", whose weights are 0
       for (int x = tid; x < T::PARTS; x += kThreads)
         *reinterpret_cast<v4u32*>(vl + (VSLOTS - 1) * BYTES + x * 16) = v4u32{0, 0, 0, 0};
-      fetch(kbase, kstride, 1, e1, kr);
+      fetch(kbase, x1.k, kr);
       put_k(BYTES, kr);
     }
     __syncthreads();
@@ -468,30 +497,28 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     auto next = [](int slot, int slots) { return slot == (slots - 1) * BYTES ? 0 : slot + BYTES; };
     if (T::PIPE) scores(0, sa);
     auto step = [&](int i, f32x16& cur, f32x16& nxt, weights& p, weights& pn) __attribute__((always_inline)) {
-      check_entries(raw, e2);
-      fetch(kbase, kstride, i + AHEAD, AHEAD == 2 ? e2 : e1, kr);
-      fetch(vbase, vstride, i + 1, e1, vr);
-      read_entries(i + 3, raw);
+      look_up(i + 2, x2);
+      fetch(kbase, AHEAD == 2 ? x2.k : x1.k, kr);
+      fetch(vbase, x1.v, vr);
       float al;
       if (!T::PIPE) scores(kread, cur);
-      if (!whole(i, e0, full_lo, full_hi)) mask(i, e0, cur);
+      if (!whole(i, x0.ok, full_lo, full_hi)) mask(i, x0.ok, cur);
       if (T::PIPE) {
         scores(kread, nxt);
         softmax(cur, pn, al);
         add_values<MT, D>(vl + vread, lane, p, acc);
-        add_odd(i - 1, ep);
+        add_odd(i - 1, okp);
         rescale(al);
       } else {
         softmax(cur, pn, al);
         rescale(al);
         add_values<MT, D>(vl + vread, lane, pn, acc);
-        add_odd(i, e0);
+        add_odd(i, x0.ok);
       }
       put_k(kput, kr);
-      put_v(i + 1, vput, e1, vr);
+      put_v(i + 1, vput, x1.ok, vr);
       kread = next(kread, KSLOTS), kput = next(kput, KSLOTS), vread = next(vread, VSLOTS), vput = next(vput, VSLOTS);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) ep[t] = e0[t], e0[t] = e1[t], e1[t] = e2[t];
+      okp = x0.ok, x0 = x1, x1 = x2;
       lds_barrier();
     };
     if constexpr (T::PIPE) {
@@ -506,7 +533,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         pa = pb;
       }
       add_values<MT, D>(vl + vread, lane, pa, acc);
-      add_odd(nb - 1, ep);
+      add_odd(nb - 1, okp);
     } else {
 #pragma unroll 1
       for (int i = 0; i < nb; ++i) step(i, sa, sa, pa, pa);
