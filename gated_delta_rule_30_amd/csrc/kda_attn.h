@@ -52,11 +52,9 @@ __device__ __forceinline__ float across16(float x, F f) {
 struct MaxOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
-// Largest of three in one instruction (fmaxf would first quiet each operand's NaN).
+// Largest of three, NaN if one is (v_maximum3_f32; fmaxf would first quiet each operand's NaN).
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 __device__ __forceinline__ float across32_max(float x) {
   const unsigned u = __builtin_bit_cast(unsigned, x);
@@ -84,12 +82,13 @@ template <> __device__ __forceinline__ bool any_nonfinite<float>(v4u32 x) {
   return r;
 }
 template <> __device__ __forceinline__ bool any_nonfinite<bf16>(v4u32 x) {
-  bool r = false;
+  // an exponent of all ones carries into the sign's place
+  unsigned r = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
-  return r;
+  for (int i = 0; i < 4; ++i) r |= (x[i] & 0x7f807f80u) + 0x00800080u;
+  return (r & 0x80008000u) != 0;
 }
+
 // 16 bytes of elements, infinities and NaN as 0.
 template <typename T> __device__ __forceinline__ v4u32 finite_part(v4u32 x);
 template <> __device__ __forceinline__ v4u32 finite_part<float>(v4u32 x) {

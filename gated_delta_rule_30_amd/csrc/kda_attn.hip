@@ -43,12 +43,13 @@ struct Row {
 };
 
 // Byte offset of 16-byte part `part` of row `row` of a block's values in LDS. Parts are permuted
-// within a row so that the transposed reads of a 16-lane group (bf16: 4 rows x 2 parts; fp32: one
-// channel run in 4 rows of 4) touch every bank once.
+// within a row so that what is read at once lies in different banks (64 of 4 bytes): two parts of eight
+// rows (fp32: four parts of four rows, four apart).
 template <typename MT, int D>
 __device__ __forceinline__ int v_at(int row, int part) {
-  const int sw = sizeof(MT) == 2 ? (row & 3) << 1 : ((row >> 2) & 3) << 2;
-  return row * (D * (int)sizeof(MT)) + (part ^ sw) * 16;
+  constexpr int RC = D * (int)sizeof(MT) / 16;
+  const int sw = sizeof(MT) == 4 ? ((row >> 2) & 3) << 2 : RC >= 16 ? (row & 7) << 1 : ((row >> 1) & 3) << 1;
+  return row * (RC * 16) + (part ^ sw) * 16;
 }
 
 // Fragment of V^T: channels 16 c .. + 15, the block's keys.

@@ -11,9 +11,6 @@
 //    both operands share it, so no weight moves between lanes.
 //  - 64 rows per wave halve the LDS reads per flop: with 32, four waves read 128 bytes per clock
 //    at the full matrix rate, all that LDS gives.
-//  - One wave per SIMD has nothing else to hide behind, so three steps run side by side: the scores of the
-//    next 32 keys and the output of the last 32 on the matrix cores, the softmax of these 32 on the
-//    vector units.
 //  - The output is rescaled only when a maximum grows by more than 2^8: weights up to 2^8 cost
 //    neither the fp32 sums nor the bf16 weights any relative accuracy.
 //  - The tiles' keys are laid end to end and cut into equal shares, one per workgroup; a tile
@@ -38,24 +35,23 @@ struct Tile {
   static constexpr int NL = (PARTS + THREADS - 1) / THREADS;  // 16-byte loads per thread of them
   static constexpr int SF = RC / 2;                        // operand fragments of a score
   static constexpr int NC = D / 32;                        // 32-channel tiles of the output
-  // PIPE: scores of step i + 1 beside the softmax of i and the output of i - 1, with keys i .. i + 2 and
-  // values i - 1 .. i + 1 in LDS; otherwise keys and values of steps i and i + 1. In fp32 the products take
-  // 25 times as long as the softmax, so there is nothing to gain.
-  static constexpr bool PIPE = ES == 2;
-  static constexpr int AHEAD = PIPE ? 2 : 1, KSLOTS = AHEAD + 1, VSLOTS = PIPE ? 3 : 2;
-  static constexpr int LDS = (KSLOTS + VSLOTS) * BYTES;
+  // keys and values of two steps each
+  static constexpr int LDS = 4 * BYTES;
 };
 
-// The parts of a row are permuted in LDS: a key fragment is the same part of 32 rows, a transposed value
-// fragment two parts of four rows (fp32: 32 channels of two rows), each without bank conflicts.
+// The parts of a row are permuted in LDS so that what is read at once lies in different banks
+// (64 of 4 bytes): a key fragment is the same part of 16 rows, a transposed value fragment four parts of four
+// rows (fp32: 32 channels of two rows).
 template <typename MT, int D>
 __device__ __forceinline__ int k_at(int row, int part) {
-  return row * (D * (int)sizeof(MT)) + (part ^ (row & 7)) * 16;
+  constexpr int RC = D * (int)sizeof(MT) / 16;
+  return row * (RC * 16) + (part ^ (RC >= 16 ? row & 15 : (row >> 1) & 7)) * 16;
 }
 template <typename MT, int D>
 __device__ __forceinline__ int v_at(int row, int part) {
-  const int sw = sizeof(MT) == 2 ? (row & 3) << 1 : ((row >> 2) & 1) << 3;
-  return row * (D * (int)sizeof(MT)) + (part ^ sw) * 16;
+  constexpr int RC = D * (int)sizeof(MT) / 16;
+  const int sw = sizeof(MT) == 4 ? ((row >> 2) & 1) << 3 : RC >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+  return row * (RC * 16) + (part ^ sw) * 16;
 }
 
 // Lane l is (m = l % 32, h = l / 32). In a 32 x 32 result it holds column m, rows
@@ -195,18 +191,38 @@ __device__ __forceinline__ AttnArgs fresh_args() {
   return *(const AttnArgs*)(const void*)p;
 }
 
+// x in scalar registers of its own: a value that is a part of loaded arguments keeps all of the registers
+// that they were loaded to.
+template <typename X>
+__device__ __forceinline__ X own(X x) {
+  static_assert(sizeof(X) == 4 || sizeof(X) == 8, "");
+  if constexpr (sizeof(X) == 4) {
+    return __builtin_bit_cast(X, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)u), hi = __builtin_amdgcn_readfirstlane((unsigned)(u >> 32));
+    return __builtin_bit_cast(X, (uint64_t)hi << 32 | lo);
+  }
+}
+
+// A pointer to global memory (that has been through `own`, it would be taken for one to any).
+template <typename X>
+__device__ __forceinline__ const __attribute__((address_space(1))) X* global(const void* p) {
+  return (const __attribute__((address_space(1))) X*)p;
+}
+
 template <typename MT, int D>
 __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD)) void tile_kernel(AttnArgs) {
   typedef Tile<MT, D> T;
   typedef typename Op<MT>::weights weights;
   constexpr int kThreads = T::THREADS, kWaves = T::WAVES, kGroups = T::S::GROUPS, ROWS = T::ROWS;
   constexpr int RC = T::RC, NL = T::NL, SF = T::SF, NC = T::NC, ES = T::ES, BYTES = T::BYTES;
-  constexpr int KSLOTS = T::KSLOTS, VSLOTS = T::VSLOTS, AHEAD = T::AHEAD;
+  constexpr bool TURNS = kWaves == 8;  // two waves per SIMD of this workgroup
   __shared__ __align__(16) char lds[T::LDS];
-  __shared__ int odd_at[VSLOTS][kWaves], counts[kWaves];
+  __shared__ int counts[kWaves];
   __shared__ Walk walk;
   char* const kl = lds;
-  char* const vl = lds + KSLOTS * BYTES;
+  char* const vl = lds + 2 * BYTES;
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 31, h2 = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int share = (blockIdx.x % 8) * (kGroups / 8) + blockIdx.x / 8;
@@ -263,7 +279,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const int n = __builtin_amdgcn_readfirstlane(walk.n), h = __builtin_amdgcn_readfirstlane(walk.h),
               tile = __builtin_amdgcn_readfirstlane(walk.tile), off = __builtin_amdgcn_readfirstlane(walk.off);
     const int left = __builtin_amdgcn_readfirstlane((int)min(walk.end - walk.at, (int64_t)INT32_MAX));
-    const int G = a.num_q_heads / a.num_kv_heads, ps1 = a.b.page_size - 1, shift = __builtin_ctz(a.b.page_size);
+    const int G = a.num_q_heads / a.num_kv_heads;
     const Seq s = seq_at(a, n, G, SUB);
     const TileKeys tk = tile_keys(a, s, tile, G);
     const int nb = min(tk.units - off, left);  // steps
@@ -273,41 +289,35 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       continue;
     }
 
-    // --- the wave's rows: lane m's query and its visible keys plo .. phi; the ranges that every row of the
-    // wave sees (full), and that some (any) and every row of the workgroup sees
-    const int row = tile * ROWS + wave * 32 + m;
-    const bool has = row < s.rows;
-    int plo, phi;
+    // --- the wave's rows: lane m's query and its visible keys vlo .. vlo + span; and the steps full_lo ..
+    // full_lo + full_n - 1 that every row of the wave sees whole
+    const int key0 = tk.lo + off * SUB, hi_key = own(min(s.hi, key0 + nb * SUB));
+    int vlo, span, full_lo, full_n;
     v4u32 qf[SF];
     {
+      const int row = tile * ROWS + wave * 32 + m;
+      const bool has = row < s.rows;
       const int tok = has ? row / G : 0, hq = h * G + (has ? row - tok * G : 0), p = s.p0 + tok;
-      phi = has ? min(p, s.hi - 1) : -1;
-      plo = a.window ? max(0, p - a.window + 1) : 0;
+      const int phi = has ? min(p, s.hi - 1) : -1, plo = a.window ? max(0, p - a.window + 1) : 0;
       const char* src = (const char*)((const MT*)a.q + (s.row0 + tok) * a.q_stride + hq * D) + h2 * 16;
 #pragma unroll
       for (int i = 0; i < SF; ++i) qf[i] = *reinterpret_cast<const v4u32*>(src + 32 * i);
-    }
-    int full_lo = has ? plo : 0, full_hi = has ? phi : INT32_MAX;
+      vlo = phi >= plo ? plo : INT32_MAX;  // (nothing: no key is at or above that)
+      span = max(0, phi - plo);
+      int lo = has ? plo : 0, hi = has ? phi : INT32_MAX;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      full_lo = max(full_lo, __shfl_xor(full_lo, d));
-      full_hi = min(full_hi, __shfl_xor(full_hi, d));
+      for (int d = 1; d < 32; d <<= 1) {
+        lo = max(lo, __shfl_xor(lo, d));
+        hi = min(hi, __shfl_xor(hi, d));
+      }
+      lo = max(0, lo - key0 + SUB - 1) / SUB;
+      hi = hi >= key0 ? (int)(((int64_t)hi - key0 + 1) / SUB) : 0;
+      full_lo = own(lo);
+      full_n = own(max(0, hi - lo));
     }
-    full_lo = __builtin_amdgcn_readfirstlane(full_lo);
-    full_hi = __builtin_amdgcn_readfirstlane(full_hi);
-    // rows of the tile run over consecutive tokens, so its ranges follow from the first and last
-    const int last = (int)((min((int64_t)(tile + 1) * ROWS, (int64_t)s.rows) - 1) / G);
-    const int pf = s.p0 + (int)((int64_t)tile * ROWS / G), pe = s.p0 + last;
-    const int w_any_hi = min(pe, s.hi - 1), w_full_hi = min(pf, s.hi - 1);
-    const int w_any_lo = a.window ? max(0, pf - a.window + 1) : 0, w_full_lo = a.window ? max(0, pe - a.window + 1) : 0;
-
-    const int32_t* table = a.b.block_table + n * a.b.table_stride;
-    const int num_pages = a.b.num_pages;
-    const int key0 = tk.lo + off * SUB, hi_key = min(s.hi, key0 + nb * SUB);
-    const int64_t kstride = a.k_page_stride * ES, vstride = a.v_page_stride * ES;
-    const char* const kbase = a.k_pages + (int64_t)h * (ps1 + 1) * D * ES;
-    const char* const vbase = a.v_pages + (int64_t)h * (ps1 + 1) * D * ES;
-    const float c = a.scale * LOG2E, slack = 8.f / c;
+    const char* const kbase = own(a.k_pages + (int64_t)h * a.b.page_size * D * ES);
+    const char* const vbase = own(a.v_pages + (int64_t)h * a.b.page_size * D * ES);
+    const float c = own(a.scale * LOG2E), slack = 8.f / c;
 
     // --- staging: a step's keys and values, thread by thread in 16-byte parts. A wave's parts lie in
     // one 16-key group of the step, or (GRPS 2) half of them in each; a group lies in one page.
@@ -319,42 +329,43 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     uint64_t pages[2];
     int ahead[2];
     auto read_table = [&](int block) __attribute__((always_inline)) {
+      const AttnArgs a = fresh_args();
+      const int32_t* table = a.b.block_table + walk.n * a.b.table_stride;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int key = key0 + (block * 64 + lane) * SUB + 16 * t;
-        ahead[t] = key < hi_key ? table[key >> shift] : -1;
+        ahead[t] = key < hi_key ? table[key >> __builtin_ctz(a.b.page_size)] : -1;
       }
     };
     auto take_table = [&](int block) __attribute__((always_inline)) {
+      const AttnArgs a = fresh_args();
 #pragma unroll
-      for (int t = 0; t < 2; ++t) pages[t] = __ballot(page_ok(ahead[t], num_pages));
+      for (int t = 0; t < 2; ++t) pages[t] = __ballot(page_ok(ahead[t], a.b.num_pages));
 #pragma unroll
       for (int g = 0; g < GRPS; ++g) {
         const int t = GRPS == 2 ? g : grp0, key = key0 + (block * 64 + lane) * SUB + 16 * t;
         const int x = t ? ahead[1] : ahead[0];
-        const int64_t page = page_ok(x, num_pages) ? x : 0, in = (key & ps1) * (D * ES);
-        kat[g] = page * kstride + in;
-        vat[g] = page * vstride + in;
+        const int64_t page = page_ok(x, a.b.num_pages) ? x : 0, in = (key & (a.b.page_size - 1)) * D;
+        kat[g] = (page * a.k_page_stride + in) * ES;
+        vat[g] = (page * a.v_page_stride + in) * ES;
       }
     };
     auto lane64 = [&](int64_t x, int l) __attribute__((always_inline)) {
       const unsigned lo = __builtin_amdgcn_readlane((unsigned)x, l), hi = __builtin_amdgcn_readlane((unsigned)(x >> 32), l);
       return (int64_t)((uint64_t)hi << 32 | lo);
     };
-    struct Step {
-      int64_t k[GRPS], v[GRPS];
-      int ok;  // bit t: the page of group t exists
-    };
-    // where step i lies (called for i = 0, 1, 2, ..)
-    auto look_up = [&](int i, Step& x) __attribute__((always_inline)) {
+    // where step i lies, and into `ok` (two bits a step, the latest lowest) whether its pages exist; called for
+    // i = 0, 1, 2, ..
+    unsigned ok = 0;
+    auto look_up = [&](int i, int64_t (&k)[GRPS], int64_t (&v)[GRPS]) __attribute__((always_inline)) {
       const int l = i & 63;
       if (l == 0) {
         take_table(i >> 6);
         read_table((i >> 6) + 1);
       }
 #pragma unroll
-      for (int g = 0; g < GRPS; ++g) x.k[g] = lane64(kat[g], l), x.v[g] = lane64(vat[g], l);
-      x.ok = (int)(pages[0] >> l & 1) | (int)(pages[1] >> l & 1) << 1;
+      for (int g = 0; g < GRPS; ++g) k[g] = lane64(kat[g], l), v[g] = lane64(vat[g], l);
+      ok = ok << 2 | (unsigned)(pages[0] >> l & 1) | (unsigned)(pages[1] >> l & 1) << 1;
     };
     auto fetch = [&](const char* base, const int64_t (&at)[GRPS], v4u32 (&r)[NL]) __attribute__((always_inline)) {
 #pragma unroll
@@ -362,7 +373,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
         const int part = j * kThreads + wave * 64, g = GRPS == 2 ? part / RC / 16 : 0;  // (j alone decides it)
         const char* src = base + (GRPS == 2 && g ? at[GRPS - 1] : at[0]) + (part - (GRPS == 2 ? g : grp0) * 16 * RC) * 16;
-        r[j] = *reinterpret_cast<const v4u32*>(src + (unsigned)lane * 16u);
+        r[j] = *global<v4u32>(src + (unsigned)lane * 16u);
       }
     };
     auto put_k = [&](int slot, const v4u32 (&r)[NL]) __attribute__((always_inline)) {
@@ -373,31 +384,17 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         *reinterpret_cast<v4u32*>(kl + slot + k_at<MT, D>(x / RC, x % RC)) = r[j];
       }
     };
-    // whether a step's keys are all in the range, and none of its pages is missing
-    auto whole = [&](int i, int ok, int lo, int hi) __attribute__((always_inline)) {
-      const int kb = key0 + i * SUB;
-      return kb >= lo && kb + SUB - 1 <= hi && ok == 3;
-    };
-    // Values that no row sees become 0. So does an infinity or NaN where some row does not see it, since a
-    // weight of 0 would not hide it; the step is then marked, and the rows that do see it get it
-    // from add_odd.
-    auto put_v = [&](int i, int slot, int ok, v4u32 (&r)[NL]) __attribute__((always_inline)) {
-      if (!whole(i, ok, w_full_lo, w_full_hi)) {
-        bool odd = false;
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-          if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
-          const int x = (j * kThreads + tid) / RC, key = key0 + i * SUB + x;
-          if (key < w_any_lo || key > w_any_hi || !(ok >> (x / 16) & 1)) r[j] = v4u32{0, 0, 0, 0};
-          odd |= any_nonfinite<MT>(r[j]);
-          r[j] = finite_part<MT>(r[j]);
-        }
-        if (lane == 0) odd_at[i % VSLOTS][wave] = 0;
-        if (odd) odd_at[i % VSLOTS][wave] = 1;
-      }
+    // An infinity or NaN is put as 0: it may lie where some row does not look, and a weight of 0 would not hide it.
+    // Rows that do see one get it at the end.
+    bool odd_seen = false;
+    auto put_v = [&](int slot, v4u32 (&r)[NL]) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
         if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
+        if (__any(any_nonfinite<MT>(r[j]))) {
+          r[j] = finite_part<MT>(r[j]);
+          odd_seen = true;
+        }
         const int x = j * kThreads + tid;
         *reinterpret_cast<v4u32*>(vl + slot + v_at<MT, D>(x / RC, x % RC)) = r[j];
       }
@@ -411,12 +408,13 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       for (int f = 0; f < SF; ++f)
         st = Op<MT>::score(*reinterpret_cast<const v4u32*>(kl + slot + k_at<MT, D>(m, 2 * f + h2)), qf[f], st);
     };
-    auto mask = [&](int i, int ok, f32x16& st) __attribute__((always_inline)) {
-      const int kb = key0 + i * SUB + 4 * h2;
+    auto mask = [&](int i, unsigned ok, f32x16& st) __attribute__((always_inline)) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int key = kb + 8 * (r / 4) + r % 4;
-        if ((key < plo) | (key > phi) | !(ok >> (r / 8) & 1)) st[r] = -INFINITY;
+      for (int t = 0; t < 2; ++t) {
+        const unsigned at = ok >> t & 1 ? (unsigned)(key0 + i * SUB + 4 * h2 + 16 * t - vlo) : 0xc0000000u;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (at + (unsigned)(8 * (r / 4) + r % 4) > (unsigned)span) st[8 * t + r] = -INFINITY;
       }
     };
     // softmax of one step: weights, running maximum and sum, and the factor for the output
@@ -448,95 +446,132 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         for (int x = 0; x < NC; ++x) acc[x] *= al;
       }
     };
-    auto add_odd = [&](int i, int ok) __attribute__((always_inline)) {
-      if (i >= 0 && !whole(i, ok, w_full_lo, w_full_hi)) {
-        bool odd = false;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) odd |= odd_at[i % VSLOTS][w] != 0;
-        if (__any(odd)) {
-#pragma unroll 1
-          for (int x = 0; x < SUB; ++x) {
-            const int key = key0 + i * SUB + x;
-            if (key > w_any_hi || !(ok >> (x / 16) & 1)) continue;
-            const MT* v = (const MT*)(vbase + table[key >> shift] * vstride) + (key & ps1) * D;
-#pragma unroll
-            for (int y = 0; y < NC * 16; ++y) {
-              const float f = (float)v[32 * (y / 16) + 8 * (y / 4 % 4) + 4 * h2 + y % 4];
-              if (f - f != 0.f && key >= plo && key <= phi) acc[y / 16][y % 16] += f;
-            }
-          }
-        }
-      }
+    auto masked = [&](int i, unsigned ok) __attribute__((always_inline)) {
+      return (unsigned)(i - full_lo) >= (unsigned)full_n || (ok & 3) != 3;
     };
-
-    // --- the steps. During step i the keys of i + AHEAD and the values of i + 1 are fetched, and put
-    // in LDS at its end. (Behind the last step the fetches read page 0, and the scores are of what lies in
-    // LDS: nobody reads either.)
-    v4u32 kr[NL], vr[NL];
-    Step x0, x1, x2;   // steps i, i + 1, i + 2
-    int okp = 0;       // x.ok of step i - 1
-    read_table(0);
-    look_up(0, x0);
-    look_up(1, x1);
-    fetch(kbase, x0.k, kr);
-    fetch(vbase, x0.v, vr);
-    put_k(0, kr);
-    put_v(0, 0, x0.ok, vr);
-    if (T::PIPE) {
+    weights p = {};
+    if constexpr (TURNS) {
+      // --- the steps. Scores of step i and values of step i - 1 are one phase, the softmax of i the next. Of
+      // the two waves on a SIMD one is a phase behind the other: one has the matrix core while the
+      // other has the vector unit. Keys of step i + 1 and values of step i come to LDS while the first wave is in
+      // its softmax of i and the second in its products of i; they were fetched two steps before. (Behind the
+      // last step the fetches read page 0, which nobody uses.)
+      v4u32 k0[NL], v0[NL], k1[NL], v1[NL];
+      int64_t xk[GRPS], xv[GRPS], yv[GRPS], zv[GRPS];  // where keys and values of the latest steps lie
+      read_table(0);
+      look_up(0, xk, zv);
+      fetch(kbase, xk, k0);
+      put_k(0, k0);
+      look_up(1, xk, yv);
+      fetch(kbase, xk, k0);
+      fetch(vbase, zv, v0);
+      look_up(2, xk, xv);
+      fetch(kbase, xk, k1);
+      fetch(vbase, yv, v1);
       // "step -1", whose weights are 0
-      for (int x = tid; x < T::PARTS; x += kThreads)
-        *reinterpret_cast<v4u32*>(vl + (VSLOTS - 1) * BYTES + x * 16) = v4u32{0, 0, 0, 0};
-      fetch(kbase, x1.k, kr);
-      put_k(BYTES, kr);
-    }
-    __syncthreads();
-    weights pa = {}, pb;
-    f32x16 sa, sb;
-    // slots: of the next step's scores or (not PIPE) this one's, of what is put, of the values
-    int kread = T::PIPE ? BYTES : 0, kput = AHEAD % KSLOTS * BYTES, vread = T::PIPE ? (VSLOTS - 1) * BYTES : 0, vput = BYTES;
-    auto next = [](int slot, int slots) { return slot == (slots - 1) * BYTES ? 0 : slot + BYTES; };
-    if (T::PIPE) scores(0, sa);
-    auto step = [&](int i, f32x16& cur, f32x16& nxt, weights& p, weights& pn) __attribute__((always_inline)) {
-      look_up(i + 2, x2);
-      fetch(kbase, AHEAD == 2 ? x2.k : x1.k, kr);
-      fetch(vbase, x1.v, vr);
-      float al;
-      if (!T::PIPE) scores(kread, cur);
-      if (!whole(i, x0.ok, full_lo, full_hi)) mask(i, x0.ok, cur);
-      if (T::PIPE) {
-        scores(kread, nxt);
-        softmax(cur, pn, al);
-        add_values<MT, D>(vl + vread, lane, p, acc);
-        add_odd(i - 1, okp);
-        rescale(al);
-      } else {
-        softmax(cur, pn, al);
-        rescale(al);
-        add_values<MT, D>(vl + vread, lane, pn, acc);
-        add_odd(i, x0.ok);
-      }
-      put_k(kput, kr);
-      put_v(i + 1, vput, x1.ok, vr);
-      kread = next(kread, KSLOTS), kput = next(kput, KSLOTS), vread = next(vread, VSLOTS), vput = next(vput, VSLOTS);
-      okp = x0.ok, x0 = x1, x1 = x2;
+      for (int x = tid; x < T::PARTS; x += kThreads) *reinterpret_cast<v4u32*>(vl + BYTES + x * 16) = v4u32{0, 0, 0, 0};
       lds_barrier();
-    };
-    if constexpr (T::PIPE) {
+      const bool second = wave >= kWaves / 2;
+      if (second) lds_barrier();
+      // ODD: i & 1
+      auto step = [&](int i, auto ODD, v4u32 (&kf)[NL], v4u32 (&vf)[NL]) __attribute__((always_inline)) {
+        constexpr int odd = decltype(ODD)::value;
+#pragma unroll
+        for (int g = 0; g < GRPS; ++g) yv[g] = xv[g];
+        look_up(i + 3, xk, xv);  // `ok` ends at step i + 3 from here on
+        auto put = [&]() __attribute__((always_inline)) {
+          put_k((1 - odd) * BYTES, kf);
+          put_v(odd * BYTES, vf);
+          fetch(kbase, xk, kf);
+          fetch(vbase, yv, vf);
+        };
+        // all of the phase's fragments are on their way before its first product: waiting for each in
+        // turn costs more than the products
+        f32x16 st = {};
+        decltype(value_frag<D>(vl, lane, 0, 0, MT())) vfr[Op<MT>::NF][NC];
+        v4u32 kfr[SF];
+#pragma unroll
+        for (int f = 0; f < Op<MT>::NF; ++f)
+#pragma unroll
+          for (int x = 0; x < NC; ++x) vfr[f][x] = value_frag<D>(vl + (1 - odd) * BYTES, lane, f, x, MT());
+#pragma unroll
+        for (int f = 0; f < SF; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + odd * BYTES + k_at<MT, D>(m, 2 * f + h2));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < Op<MT>::NF; ++f)
+#pragma unroll
+          for (int x = 0; x < NC; ++x) acc[x] = Op<MT>::value(vfr[f][x], p, f, acc[x]);
+#pragma unroll
+        for (int f = 0; f < SF; ++f) st = Op<MT>::score(kfr[f], qf[f], st);
+        if (second) put();
+        lds_barrier();
+        if (masked(i, ok >> 6)) mask(i, ok >> 6, st);
+        float al;
+        softmax(st, p, al);
+        rescale(al);
+        if (!second) put();
+        lds_barrier();
+      };
       int i = 0;
 #pragma unroll 1
       for (; i + 1 < nb; i += 2) {
-        step(i, sa, sb, pa, pb);
-        step(i + 1, sb, sa, pb, pa);
+        step(i, std::integral_constant<int, 0>(), k0, v0);
+        step(i + 1, std::integral_constant<int, 1>(), k1, v1);
       }
-      if (i < nb) {
-        step(i, sa, sb, pa, pb);
-        pa = pb;
-      }
-      add_values<MT, D>(vl + vread, lane, pa, acc);
-      add_odd(nb - 1, okp);
+      if (i < nb) step(i, std::integral_constant<int, 0>(), k0, v0);
+      if (!second) lds_barrier();
+      add_values<MT, D>(vl + ((nb - 1) & 1) * BYTES, lane, p, acc);
     } else {
+      // --- the steps, one wave per SIMD of this workgroup: step i's products and softmax in turn, the next step's
+      // keys and values fetched meanwhile and put in LDS at the end
+      v4u32 kf[NL], vf[NL];
+      int64_t xk[GRPS], xv[GRPS];
+      read_table(0);
+      look_up(0, xk, xv);
+      fetch(kbase, xk, kf);
+      fetch(vbase, xv, vf);
+      put_k(0, kf);
+      put_v(0, vf);
+      lds_barrier();
 #pragma unroll 1
-      for (int i = 0; i < nb; ++i) step(i, sa, sa, pa, pa);
+      for (int i = 0; i < nb; ++i) {
+        const int slot = (i & 1) * BYTES;
+        look_up(i + 1, xk, xv);
+        fetch(kbase, xk, kf);
+        fetch(vbase, xv, vf);
+        f32x16 st;
+        float al;
+        scores(slot, st);
+        if (masked(i, ok >> 2)) mask(i, ok >> 2, st);
+        softmax(st, p, al);
+        rescale(al);
+        add_values<MT, D>(vl + slot, lane, p, acc);
+        put_k(BYTES - slot, kf);
+        put_v(BYTES - slot, vf);
+        lds_barrier();
+      }
+    }
+
+    // --- the rows that see an infinity or NaN among the values gain it
+    if (tid == 0) counts[0] = 0;
+    __syncthreads();
+    if (odd_seen) counts[0] = 1;
+    __syncthreads();
+    if (counts[0]) {
+      const AttnArgs a = fresh_args();
+      const int32_t* table = a.b.block_table + walk.n * a.b.table_stride;
+      const int ps = a.b.page_size;
+#pragma unroll 1
+      for (int key = key0; key < hi_key; ++key) {
+        const int pg = table[key / ps];
+        if (!page_ok(pg, a.b.num_pages) || (unsigned)(key - vlo) > (unsigned)span) continue;
+        const MT* v = (const MT*)a.v_pages + pg * a.v_page_stride + ((int64_t)walk.h * ps + key % ps) * D;
+#pragma unroll
+        for (int y = 0; y < NC * 16; ++y) {
+          const float f = (float)v[32 * (y / 16) + 8 * (y / 4 % 4) + 4 * h2 + y % 4];
+          if (f - f != 0.f) acc[y / 16][y % 16] += f;
+        }
+      }
     }
 
     // --- out

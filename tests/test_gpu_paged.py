@@ -295,11 +295,14 @@ def test_append_in_place_and_nowhere():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_same_bits_every_run(dtype):
-    s = make([1, 60, 1, 3], [900, 30, 2000, 77], 8, 2, 128, 16, dtype, seed=13)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,ctx", [([1, 60, 1, 3], [900, 30, 2000, 77]), ([400], [700]), ([40], [11]),
+                                     ([1, 1, 1], [900, 17, 2000])])
+def test_same_bits_every_run(new, ctx, D, dtype):
+    s = make(new, ctx, 8, 2, D, 16, dtype, seed=13)
     d = dev(s)
     a = run(d)
-    for _ in range(3):
+    for _ in range(5):
         b = run(d)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
