@@ -6,6 +6,17 @@
 
 namespace kda {
 
+// An item (the rows of one tile, over all their keys) that is cut between workgroups: its number of
+// units and the first one's place among all. The workgroup that has its first part writes this, or n = -1 if
+// there is none; every part leaves its sums in the workspace, and the join kernel adds them up.
+struct Cut {
+  int64_t at;
+  int32_t n, h, tile, units;
+};
+// Part of workgroup w of an item that starts at `at`, in shares of `per` units: a workgroup leaves at most
+// two, of the item that it starts with and of the one it ends with.
+__host__ __device__ inline int64_t part_of(int64_t w, int64_t at, int64_t per) { return 2 * w + (at > w * per); }
+
 // First row of sequence n's new tokens (n = num_seqs: one past the last), clamped to the rows.
 __device__ __forceinline__ int64_t first_row(const PagedBatch& b, int n) {
   if (!b.cu_seqlens) return b.total_tokens / b.num_seqs * n;
@@ -152,17 +163,20 @@ constexpr int attn_tile_groups(int D, bool bf16) {
 
 struct TilePlan {
   int64_t *pre, *tile_first;
+  Cut* cut;     // of each workgroup
   float* part;  // two partial results per workgroup: tile_rows rows of D sums, then m and l of each
 };
 __host__ __device__ inline int64_t max_tiles(int num_seqs, int64_t total_tokens, int G, int tile_rows) {
   return total_tokens * G / tile_rows + num_seqs;
 }
+constexpr int kMaxTileGroups = 512;
 __host__ __device__ inline size_t tile_plan_bytes(int num_seqs, int64_t tiles) {
-  return ((size_t)(tiles + 1 + num_seqs + 1) * 8 + 255) / 256 * 256;
+  return (sizeof(Cut) * kMaxTileGroups + (size_t)(tiles + 1 + num_seqs + 1) * 8 + 255) / 256 * 256;
 }
 __host__ __device__ inline TilePlan tile_plan_at(char* ws, int num_seqs, int64_t tiles) {
   TilePlan p;
-  p.tile_first = reinterpret_cast<int64_t*>(ws);
+  p.cut = reinterpret_cast<Cut*>(ws);
+  p.tile_first = reinterpret_cast<int64_t*>(p.cut + kMaxTileGroups);
   p.pre = p.tile_first + num_seqs + 1;
   p.part = reinterpret_cast<float*>(ws + tile_plan_bytes(num_seqs, tiles));
   return p;
@@ -180,11 +194,76 @@ __device__ __forceinline__ TileKeys tile_keys(const AttnArgs& a, const Seq& s, i
   k.hi = (int)min((int64_t)s.hi, (int64_t)s.p0 + i1 + 1);
   const int64_t lo = a.window ? (int64_t)s.p0 + i0 - a.window + 1 : 0;
   k.lo = lo > 0 ? (int)(min(lo, (int64_t)INT32_MAX) / kTileUnit) * kTileUnit : 0;
-  k.units = k.hi > k.lo ? (k.hi - k.lo + kTileUnit - 1) / kTileUnit : 0;
+  // a tile without keys is computed all the same: one unit that nobody sees
+  k.units = k.hi > k.lo ? (k.hi - k.lo + kTileUnit - 1) / kTileUnit : 1;
   return k;
 }
 
-void launch_attn_tile(const AttnArgs& a);
+// The plan, by one workgroup of kPlanThreads threads.
+constexpr int kPlanThreads = 256;
+struct PlanLds {
+  int64_t sums[kPlanThreads / 64];
+};
+__device__ __forceinline__ void make_tile_plan(const AttnArgs& a, PlanLds& lds) {
+  constexpr int kWaves = kPlanThreads / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, N = a.b.num_seqs;
+  const int G = a.num_q_heads / a.num_kv_heads;
+  const int64_t most = max_tiles(N, a.b.total_tokens, G, a.tile_rows);
+  const TilePlan pl = tile_plan_at(a.tile_ws, N, most);
+  auto scan = [&](int64_t x, int64_t* total) {  // inclusive, in thread order
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) lds.sums[wave] = x;
+    __syncthreads();
+    int64_t all = 0;
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) x += lds.sums[w];
+      all += lds.sums[w];
+    }
+    *total = all;
+    return x;
+  };
+  int64_t carry = 0, total;
+  for (int n0 = 0; n0 < N; n0 += kPlanThreads) {
+    const int n = n0 + tid;
+    int64_t tiles = 0;
+    if (n < N) {
+      const Seq s = seq_at(a, n, G, kTileUnit);
+      if (s.rows > a.row_limit) tiles = (s.rows + a.tile_rows - 1) / a.tile_rows;
+    }
+    const int64_t x = carry + scan(tiles, &total);
+    if (n < N) pl.tile_first[n] = min(most, x - tiles);
+    carry = min(most, carry + total);
+  }
+  if (tid == 0) pl.tile_first[N] = carry;
+  __syncthreads();
+  const int64_t tiles = carry;
+  carry = 0;
+  for (int64_t i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+    const int64_t i = i0 + tid;
+    int64_t units = 0;
+    if (i < tiles) {
+      int lo = 0, hi = N - 1;  // the last sequence that starts at or before tile i
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (pl.tile_first[mid] <= i) lo = mid;
+        else hi = mid - 1;
+      }
+      units = tile_keys(a, seq_at(a, lo, G, kTileUnit), (int)(i - pl.tile_first[lo]), G).units;
+    }
+    const int64_t x = carry + scan(units, &total);
+    if (i < tiles) pl.pre[i] = x - units;
+    carry += total;
+  }
+  if (tid == 0) pl.pre[tiles] = carry;
+}
+
+// plan: whether the plan has to be made first (else the row kernel's launch has made it)
+void launch_attn_tile(const AttnArgs& a, bool plan);
 size_t attn_tile_bytes(int num_seqs, int64_t total_tokens, int G, int head_dim, bool bf16);
 
 }  // namespace kda

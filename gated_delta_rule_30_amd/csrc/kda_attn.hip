@@ -71,24 +71,27 @@ __device__ __forceinline__ f32x4 v_frag(const char* v, int c, int m, int g, floa
 __device__ __forceinline__ bf16x8 p_frag(const f32x4 (&s)[2], bf16) { return frag_from_acc(s[0], s[1], bf16()); }
 __device__ __forceinline__ f32x4 p_frag(const f32x4 (&s)[1], float) { return s[0]; }
 
-// Workspace: how the work is cut, then two partial results per workgroup (an item cut at its start
-// and one cut at its end), each 16 rows of D sums, then m and l of each row.
+// Workspace: the units per workgroup, each workgroup's cut item, and its two partial results, each 16 rows
+// of D sums, then m and l of each row.
 struct Ws {
-  int64_t* split;  // [0]: units per workgroup, [1 + n]: first unit of sequence n, n = 0 .. num_seqs
+  int64_t* per;
+  Cut* cut;
   float* part;
 };
-__host__ __device__ inline size_t split_bytes(int num_seqs) {
-  return ((size_t)(num_seqs + 2) * 8 + 255) / 256 * 256;
-}
-__host__ __device__ inline Ws ws_at(char* ws, int num_seqs) {
-  return {reinterpret_cast<int64_t*>(ws), reinterpret_cast<float*>(ws + split_bytes(num_seqs))};
+__host__ __device__ inline Ws ws_at(char* ws) {
+  Ws w;
+  w.per = reinterpret_cast<int64_t*>(ws);
+  w.cut = reinterpret_cast<Cut*>(ws + 256);
+  w.part = reinterpret_cast<float*>(ws + 256 + sizeof(Cut) * kGroups);
+  return w;
 }
 constexpr int part_floats(int D) { return 16 * D + 32; }
 
-// Units of sequence n's items, all heads and tiles; none if the tile kernel takes it.
+// Units of one of a sequence's items (a tile without keys is computed all the same: one unit that nobody
+// sees), and of all of them; none if the tile kernel takes the sequence.
+__device__ __forceinline__ int item_units(const Seq& s, int unit) { return max(1, (s.hi - s.lo + unit - 1) / unit); }
 __device__ __forceinline__ int64_t seq_units(const AttnArgs& a, const Seq& s, int Hk, int unit) {
-  if (s.rows > a.row_limit) return 0;
-  return (int64_t)((s.rows + 15) / 16) * Hk * ((s.hi - s.lo + unit - 1) / unit);
+  return s.rows > a.row_limit ? 0 : (int64_t)((s.rows + 15) / 16) * Hk * item_units(s, unit);
 }
 
 template <typename MT, int D>
@@ -99,10 +102,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
   __shared__ __align__(16) char lds[R::LDS];
   __shared__ float ml[kWaves][16][2];
   __shared__ int64_t scan[kWaves], found[2];
+  __shared__ PlanLds plan;
+  if (blockIdx.x == kGroups) {  // one workgroup more, where the tile kernel is to follow
+    make_tile_plan(a, plan);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
   const int N = a.b.num_seqs, Hk = a.num_kv_heads, G = a.num_q_heads / Hk, ps = a.b.page_size,
             shift = __builtin_ctz(ps);
-  const Ws ws = ws_at(a.workspace, N);
+  const Ws ws = ws_at(a.workspace);
 
   // --- this workgroup's share [at, end) of all units: each thread adds up a run of sequences
   const int run = (N + kThreads - 1) / kThreads, n0 = min(N, tid * run), n1 = min(N, n0 + run);
@@ -123,17 +131,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
     total += scan[w];
   }
   const int64_t per = max((int64_t)1, (total + kGroups - 1) / kGroups);
-  if (blockIdx.x == 0) {
-    int64_t f = before;
-    for (int n = n0; n < n1; ++n) {
-      ws.split[1 + n] = f;
-      f += seq_units(a, seq_at(a, n, G, UNIT), Hk, UNIT);
-    }
-    if (tid == 0) ws.split[0] = per;
-    if (n0 < n1 && n1 == N) ws.split[1 + N] = f;
+  if (tid == 0) {
+    if (blockIdx.x == 0) *ws.per = per;
+    ws.cut[blockIdx.x].n = -1;
   }
   int64_t at = (int64_t)blockIdx.x * per;
-  const int64_t begin = at, end = min(total, at + per);
+  const int64_t end = min(total, at + per);
   if (at >= end) return;
   if (before <= at && at < before + mine) {
     int64_t f = before;
@@ -153,7 +156,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
   const float c = a.scale * LOG2E;
   while (at < end) {
     const Seq s = seq_at(a, n, G, UNIT);
-    const int units = (s.hi - s.lo + UNIT - 1) / UNIT, tiles = (s.rows + 15) / 16;
+    const int units = item_units(s, UNIT), tiles = (s.rows + 15) / 16;
     const int64_t all = seq_units(a, s, Hk, UNIT);
     if (at >= first + all) {
       first += all;
@@ -346,7 +349,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
       *reinterpret_cast<f32x4*>(ot + m * D + 4 * ((4 * j + g) ^ (m & 7))) = acc[j];
     __syncthreads();
     const bool done = u0 == 0 && u1 == units;
-    float* part = ws.part + (2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1)) * part_floats(D);
+    float* part = ws.part + part_of(blockIdx.x, at, per) * part_floats(D);
+    if (tid == 0 && !done && u0 == 0) ws.cut[blockIdx.x] = {at, n, h, tile, units};
 #pragma unroll
     for (int e = 0; e < 16 * D / 4 / kThreads; ++e) {
       const int i = e * kThreads + tid, r = i / (D / 4), q4 = i % (D / 4), orow = tile * 16 + r;
@@ -381,69 +385,61 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
   }
 }
 
-// Joins the parts of items that were cut, and writes the rows that have no keys: one wave per
-// (token, query head).
+// Joins the parts of the items that were cut: one workgroup per cut item of the row kernel (the first
+// row_groups workgroups), and one per 64 rows of those of the tile kernel. 16 threads a row.
 template <typename MT, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
-  typedef Row<MT, D> R;
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63, N = a.b.num_seqs, Hk = a.num_kv_heads, G = a.num_q_heads / Hk;
-  const int64_t out = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (out >= a.b.total_tokens * a.num_q_heads) return;
-  const int64_t t = out / a.num_q_heads;
-  const int hq = (int)(out - t * a.num_q_heads), h = hq / G;
-  // the token's sequence: the boundaries at or below it, counted over the lanes
-  int n = 0;
-  if (a.b.cu_seqlens) {
-    for (int i = lane; i < N; i += 64) n += first_row(a.b, i + 1) <= t;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-    if (n == N || t < first_row(a.b, 0)) return;
-  } else {
-    n = (int)(t / (a.b.total_tokens / N));
-  }
-  // its item: units b .. e - 1 of the kernel that computed it, in shares of `per`
-  const Seq s = seq_at(a, n, G, R::UNIT);
-  const int row = (int)(t - s.row0) * G + hq - h * G;
-  int64_t per, b, e;
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int row_groups) {
+  typedef TileShape<D, sizeof(MT) == 2> S;
+  constexpr int E = D / 64;  // vectors of 4 channels per thread, 16 threads apart
+  const int N = a.b.num_seqs, G = a.num_q_heads / a.num_kv_heads;
+  const bool tiled = (int)blockIdx.x >= row_groups;
+  const int w = tiled ? ((int)blockIdx.x - row_groups) / (S::ROWS / 64) : blockIdx.x;
+  Cut cut;
   const float* parts;
-  int64_t size;
-  int r, rows;  // the row within its tile, and the tile's rows
-  if (s.rows > a.row_limit) {
-    const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, a.tile_rows));
-    const int64_t t0 = pl.tile_first[n], i = t0 + row / a.tile_rows;
-    per = max((int64_t)1, (Hk * pl.pre[pl.tile_first[N]] + TileShape<D, sizeof(MT) == 2>::GROUPS - 1) / TileShape<D, sizeof(MT) == 2>::GROUPS);
-    b = Hk * pl.pre[t0] + h * (pl.pre[pl.tile_first[n + 1]] - pl.pre[t0]) + pl.pre[i] - pl.pre[t0];
-    e = b + pl.pre[i + 1] - pl.pre[i];
-    parts = pl.part, rows = a.tile_rows, size = tile_part_floats(rows, D), r = row % rows;
+  int64_t per, size;
+  int rows, r0 = 0;
+  if (tiled) {
+    const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, S::ROWS));
+    cut = pl.cut[w];
+    if (cut.n < 0) return;
+    per = max((int64_t)1, (a.num_kv_heads * pl.pre[pl.tile_first[N]] + S::GROUPS - 1) / S::GROUPS);
+    parts = pl.part, rows = S::ROWS, size = tile_part_floats(S::ROWS, D);
+    r0 = ((int)blockIdx.x - row_groups) % (S::ROWS / 64) * 64;
   } else {
-    const Ws ws = ws_at(a.workspace, N);
-    const int units = (s.hi - s.lo + R::UNIT - 1) / R::UNIT;
-    per = ws.split[0];
-    b = ws.split[1 + n] + ((int64_t)h * ((s.rows + 15) / 16) + row / 16) * units;
-    e = b + units;
-    parts = ws.part, rows = 16, size = part_floats(D), r = row & 15;
+    const Ws ws = ws_at(a.workspace);
+    cut = ws.cut[w];
+    if (cut.n < 0) return;
+    per = *ws.per;
+    parts = ws.part, rows = 16, size = part_floats(D);
   }
-  float o[E] = {}, M = -INFINITY, l = 0.f;
-  if (e > b) {
-    const int64_t w0 = b / per, w1 = (e - 1) / per;
-    if (w0 == w1) return;  // written by its one workgroup
-    const float c = a.scale * LOG2E;
-    for (int64_t w = w0; w <= w1; ++w) {
-      const float* part = parts + (2 * w + (w == w0 && b != w * per)) * size;
-      const float pm = part[rows * D + 2 * r], pl = part[rows * D + 2 * r + 1];
+  const int64_t row0 = first_row(a.b, cut.n);
+  const int64_t all = (first_row(a.b, cut.n + 1) - row0) * G, last = (cut.at + cut.units - 1) / per;
+  const float c = a.scale * LOG2E;
+  const int lane = threadIdx.x & 15;
+  for (int r = r0 + threadIdx.x / 16; r < min(rows, r0 + 64); r += kThreads / 16) {
+    const int64_t row = (int64_t)cut.tile * rows + r;
+    if (row >= all) break;
+    f32x4 o[E] = {};
+    float M = -INFINITY, l = 0.f;
+    for (int64_t v = w; v <= last; ++v) {
+      const float* part = parts + part_of(v, cut.at, per) * size;
+      const float pm = part[(int64_t)rows * D + 2 * r], pl = part[(int64_t)rows * D + 2 * r + 1];
       const float mn = fmaxf(M, pm), mu = mn == -INFINITY ? 0.f : mn;
       const float al = exp2_f((M - mu) * c), be = exp2_f((pm - mu) * c);
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = o[i] * al + be * part[(int64_t)r * D + E * lane + i];
+      for (int i = 0; i < E; ++i)
+        o[i] = o[i] * al + be * *reinterpret_cast<const f32x4*>(part + (int64_t)r * D + 64 * i + 4 * lane);
       l = l * al + be * pl;
       M = mn;
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t tok = row / G, out = (row0 + tok) * a.num_q_heads + cut.h * G + row - tok * G;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int i = 0; i < E; ++i) ((MT*)a.o)[out * D + E * lane + i] = from_f32<MT>(o[i] * inv);
-  if (a.lse && lane == 0) a.lse[out] = M * a.scale + (l == 0.f ? 0.f : logf(l));
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) ((MT*)a.o)[out * D + 64 * i + 4 * lane + x] = from_f32<MT>(o[i][x] * inv);
+    if (a.lse && lane == 0) a.lse[out] = M * a.scale + (l == 0.f ? 0.f : logf(l));
+  }
 }
 
 // Which kernel takes which sequence. Without cu_seqlens every sequence has the same rows; with
@@ -466,14 +462,16 @@ Route route(int num_seqs, int64_t total_tokens, int G, bool ragged, int tile_row
 
 template <typename MT, int D>
 void launch_rows(const AttnArgs& a, bool rows) {
-  if (rows) row_kernel<MT, D><<<kGroups, kThreads, 0, a.stream>>>(a);
-  if (a.tile_rows) launch_attn_tile(a);
-  const int64_t n = a.b.total_tokens * a.num_q_heads;
-  join_kernel<MT, D><<<(unsigned)((n + kWaves - 1) / kWaves), kThreads, 0, a.stream>>>(a);
+  const bool tiles = a.tile_rows != 0;
+  if (rows) row_kernel<MT, D><<<kGroups + tiles, kThreads, 0, a.stream>>>(a);
+  if (tiles) launch_attn_tile(a, !rows);
+  typedef TileShape<D, sizeof(MT) == 2> S;
+  const int row_groups = rows ? kGroups : 0;
+  join_kernel<MT, D><<<row_groups + (tiles ? S::GROUPS * (S::ROWS / 64) : 0), kThreads, 0, a.stream>>>(a, row_groups);
 }
 
-size_t row_bytes(int num_seqs, int head_dim) {
-  return (split_bytes(num_seqs) + (size_t)2 * kGroups * part_floats(head_dim) * 4 + 255) / 256 * 256;
+size_t row_bytes(int head_dim) {
+  return (256 + sizeof(Cut) * kGroups + (size_t)2 * kGroups * part_floats(head_dim) * 4 + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -487,7 +485,7 @@ size_t attn_workspace_bytes(int num_seqs, int64_t total_tokens, int num_q_heads,
     const size_t n = r.tile_rows ? attn_tile_bytes(num_seqs, total_tokens, G, head_dim, bf16) : 0;
     tile = n > tile ? n : tile;
   }
-  return row_bytes(num_seqs, head_dim) + tile;
+  return row_bytes(head_dim) + tile;
 }
 
 hipError_t launch_attn(const AttnArgs& args) {
@@ -496,7 +494,7 @@ hipError_t launch_attn(const AttnArgs& args) {
   const Route r = route(a.b.num_seqs, a.b.total_tokens, a.num_q_heads / a.num_kv_heads, a.b.cu_seqlens != nullptr,
                         attn_tile_rows(a.head_dim, a.dtype_bf16));
   a.row_limit = r.row_limit, a.tile_rows = r.tile_rows;
-  a.tile_ws = a.workspace + row_bytes(a.b.num_seqs, a.head_dim);
+  a.tile_ws = a.workspace + row_bytes(a.head_dim);
   if (a.dtype_bf16) {
     if (a.head_dim == 64) launch_rows<bf16, 64>(a, r.rows);
     if (a.head_dim == 128) launch_rows<bf16, 128>(a, r.rows);

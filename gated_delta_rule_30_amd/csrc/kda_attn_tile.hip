@@ -118,64 +118,9 @@ __device__ __forceinline__ void add_values(const char* v, int lane, const typena
     for (int c = 0; c < D / 32; ++c) acc[c] = Op<MT>::value(value_frag<D>(v, lane, i, c, MT()), p, i, acc[c]);
 }
 
-// ------------------------------------------------------------------ the plan
-constexpr int kPlan = 1024;
-__global__ __launch_bounds__(kPlan) void tile_plan_kernel(AttnArgs a) {
-  __shared__ int64_t lds[kPlan / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, N = a.b.num_seqs;
-  const int G = a.num_q_heads / a.num_kv_heads;
-  const int64_t most = max_tiles(N, a.b.total_tokens, G, a.tile_rows);
-  const TilePlan pl = tile_plan_at(a.tile_ws, N, most);
-  auto scan = [&](int64_t x, int64_t* total) {  // inclusive, in thread order
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t y = __shfl_up(x, d);
-      if (lane >= d) x += y;
-    }
-    __syncthreads();
-    if (lane == 63) lds[wave] = x;
-    __syncthreads();
-    int64_t all = 0;
-    for (int w = 0; w < kPlan / 64; ++w) {
-      if (w < wave) x += lds[w];
-      all += lds[w];
-    }
-    *total = all;
-    return x;
-  };
-  int64_t carry = 0, total;
-  for (int n0 = 0; n0 < N; n0 += kPlan) {
-    const int n = n0 + tid;
-    int64_t tiles = 0;
-    if (n < N) {
-      const Seq s = seq_at(a, n, G, SUB);
-      if (s.rows > a.row_limit) tiles = (s.rows + a.tile_rows - 1) / a.tile_rows;
-    }
-    const int64_t x = carry + scan(tiles, &total);
-    if (n < N) pl.tile_first[n] = min(most, x - tiles);
-    carry = min(most, carry + total);
-  }
-  if (tid == 0) pl.tile_first[N] = carry;
-  __syncthreads();
-  const int64_t tiles = carry;
-  carry = 0;
-  for (int64_t i0 = 0; i0 < tiles; i0 += kPlan) {
-    const int64_t i = i0 + tid;
-    int64_t units = 0;
-    if (i < tiles) {
-      int lo = 0, hi = N - 1;  // the last sequence that starts at or before tile i
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (pl.tile_first[mid] <= i) lo = mid;
-        else hi = mid - 1;
-      }
-      units = tile_keys(a, seq_at(a, lo, G, SUB), (int)(i - pl.tile_first[lo]), G).units;
-    }
-    const int64_t x = carry + scan(units, &total);
-    if (i < tiles) pl.pre[i] = x - units;
-    carry += total;
-  }
-  if (tid == 0) pl.pre[tiles] = carry;
+__global__ __launch_bounds__(kPlanThreads) void tile_plan_kernel(AttnArgs a) {
+  __shared__ PlanLds lds;
+  make_tile_plan(a, lds);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -235,6 +180,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, ROWS));
     const int64_t total = Hk * pl.pre[pl.tile_first[N]], per = max((int64_t)1, (total + kGroups - 1) / kGroups);
     const int64_t at = share * per;
+    if (tid == 0) pl.cut[share].n = -1;
     if (at >= total) return;
     // the entries of a sorted array that are at most x, counted over the threads
     auto count = [&](int64_t n, auto entry, int64_t x) {
@@ -283,11 +229,6 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const Seq s = seq_at(a, n, G, SUB);
     const TileKeys tk = tile_keys(a, s, tile, G);
     const int nb = min(tk.units - off, left);  // steps
-    if (nb <= 0) {                             // a tile without keys
-      __syncthreads();
-      if (tid == 0) ++walk.tile, walk.off = 0;
-      continue;
-    }
 
     // --- the wave's rows: lane m's query and its visible keys vlo .. vlo + span; and the steps full_lo ..
     // full_lo + full_n - 1 that every row of the wave sees whole
@@ -599,7 +540,9 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
           if (a.lse && h2 == 0) a.lse[out] = mx * a.scale + (l == 0.f ? 0.f : logf(l));
         } else {
           const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, ROWS));
-          float* part = pl.part + (2 * (int64_t)share + (walk.at == walk.begin ? 0 : 1)) * tile_part_floats(ROWS, D);
+          const int64_t per = walk.end - walk.begin;  // (only the last share may be shorter, and nothing is cut at its end)
+          float* part = pl.part + part_of(share, walk.at, share ? walk.begin / share : per) * tile_part_floats(ROWS, D);
+          if (tid == 0 && off == 0) pl.cut[share] = {walk.at, n, h, tile, tk.units};
 #pragma unroll
           for (int x = 0; x < NC; ++x)
 #pragma unroll
@@ -622,8 +565,8 @@ void launch(const AttnArgs& a) {
 
 }  // namespace
 
-void launch_attn_tile(const AttnArgs& a) {
-  tile_plan_kernel<<<1, kPlan, 0, a.stream>>>(a);
+void launch_attn_tile(const AttnArgs& a, bool plan) {
+  if (plan) tile_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a);
   if (a.dtype_bf16) {
     if (a.head_dim == 64) launch<bf16, 64>(a);
     if (a.head_dim == 128) launch<bf16, 128>(a);
