@@ -10,7 +10,7 @@ namespace kda {
 // units and the first one's place among all. The workgroup that has its first part writes this, or n = -1 if
 // there is none; every part leaves its sums in the workspace, and the join kernel adds them up.
 struct Cut {
-  int64_t at;
+  int64_t at, per;  // per: units per workgroup
   int32_t n, h, tile, units;
 };
 // Part of workgroup w of an item that starts at `at`, in shares of `per` units: a workgroup leaves at most

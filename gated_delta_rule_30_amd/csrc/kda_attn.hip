@@ -71,19 +71,14 @@ __device__ __forceinline__ f32x4 v_frag(const char* v, int c, int m, int g, floa
 __device__ __forceinline__ bf16x8 p_frag(const f32x4 (&s)[2], bf16) { return frag_from_acc(s[0], s[1], bf16()); }
 __device__ __forceinline__ f32x4 p_frag(const f32x4 (&s)[1], float) { return s[0]; }
 
-// Workspace: the units per workgroup, each workgroup's cut item, and its two partial results, each 16 rows
+// Workspace: each workgroup's cut item, and its two partial results, each 16 rows
 // of D sums, then m and l of each row.
 struct Ws {
-  int64_t* per;
   Cut* cut;
   float* part;
 };
 __host__ __device__ inline Ws ws_at(char* ws) {
-  Ws w;
-  w.per = reinterpret_cast<int64_t*>(ws);
-  w.cut = reinterpret_cast<Cut*>(ws + 256);
-  w.part = reinterpret_cast<float*>(ws + 256 + sizeof(Cut) * kGroups);
-  return w;
+  return {reinterpret_cast<Cut*>(ws), reinterpret_cast<float*>(ws + sizeof(Cut) * kGroups)};
 }
 constexpr int part_floats(int D) { return 16 * D + 32; }
 
@@ -131,10 +126,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
     total += scan[w];
   }
   const int64_t per = max((int64_t)1, (total + kGroups - 1) / kGroups);
-  if (tid == 0) {
-    if (blockIdx.x == 0) *ws.per = per;
-    ws.cut[blockIdx.x].n = -1;
-  }
+  if (tid == 0) ws.cut[blockIdx.x].n = -1;
   int64_t at = (int64_t)blockIdx.x * per;
   const int64_t end = min(total, at + per);
   if (at >= end) return;
@@ -350,7 +342,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
     __syncthreads();
     const bool done = u0 == 0 && u1 == units;
     float* part = ws.part + part_of(blockIdx.x, at, per) * part_floats(D);
-    if (tid == 0 && !done && u0 == 0) ws.cut[blockIdx.x] = {at, n, h, tile, units};
+    if (tid == 0 && !done && u0 == 0) ws.cut[blockIdx.x] = {at, per, n, h, tile, units};
 #pragma unroll
     for (int e = 0; e < 16 * D / 4 / kThreads; ++e) {
       const int i = e * kThreads + tid, r = i / (D / 4), q4 = i % (D / 4), orow = tile * 16 + r;
@@ -386,60 +378,48 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void row_kernel(AttnArg
 }
 
 // Joins the parts of the items that were cut: one workgroup per cut item of the row kernel (the first
-// row_groups workgroups), and one per 64 rows of those of the tile kernel. 16 threads a row.
+// row_groups workgroups), and one per 16 rows of those of the tile kernel. 16 threads a row.
 template <typename MT, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int row_groups) {
   typedef TileShape<D, sizeof(MT) == 2> S;
   constexpr int E = D / 64;  // vectors of 4 channels per thread, 16 threads apart
   const int N = a.b.num_seqs, G = a.num_q_heads / a.num_kv_heads;
   const bool tiled = (int)blockIdx.x >= row_groups;
-  const int w = tiled ? ((int)blockIdx.x - row_groups) / (S::ROWS / 64) : blockIdx.x;
-  Cut cut;
-  const float* parts;
-  int64_t per, size;
-  int rows, r0 = 0;
-  if (tiled) {
-    const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, S::ROWS));
-    cut = pl.cut[w];
-    if (cut.n < 0) return;
-    per = max((int64_t)1, (a.num_kv_heads * pl.pre[pl.tile_first[N]] + S::GROUPS - 1) / S::GROUPS);
-    parts = pl.part, rows = S::ROWS, size = tile_part_floats(S::ROWS, D);
-    r0 = ((int)blockIdx.x - row_groups) % (S::ROWS / 64) * 64;
-  } else {
-    const Ws ws = ws_at(a.workspace);
-    cut = ws.cut[w];
-    if (cut.n < 0) return;
-    per = *ws.per;
-    parts = ws.part, rows = 16, size = part_floats(D);
-  }
+  const int w = tiled ? ((int)blockIdx.x - row_groups) / (S::ROWS / 16) : blockIdx.x;
+  const Ws ws = ws_at(a.workspace);
+  const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, S::ROWS));
+  const Cut cut = tiled ? pl.cut[w] : ws.cut[w];
+  if (cut.n < 0) return;
+  const float* parts = tiled ? pl.part : ws.part;
+  const int rows = tiled ? S::ROWS : 16, r0 = tiled ? ((int)blockIdx.x - row_groups) % (S::ROWS / 16) * 16 : 0;
+  const int64_t per = cut.per, size = tiled ? tile_part_floats(S::ROWS, D) : part_floats(D);
   const int64_t row0 = first_row(a.b, cut.n);
   const int64_t all = (first_row(a.b, cut.n + 1) - row0) * G, last = (cut.at + cut.units - 1) / per;
   const float c = a.scale * LOG2E;
   const int lane = threadIdx.x & 15;
-  for (int r = r0 + threadIdx.x / 16; r < min(rows, r0 + 64); r += kThreads / 16) {
-    const int64_t row = (int64_t)cut.tile * rows + r;
-    if (row >= all) break;
-    f32x4 o[E] = {};
-    float M = -INFINITY, l = 0.f;
-    for (int64_t v = w; v <= last; ++v) {
-      const float* part = parts + part_of(v, cut.at, per) * size;
-      const float pm = part[(int64_t)rows * D + 2 * r], pl = part[(int64_t)rows * D + 2 * r + 1];
-      const float mn = fmaxf(M, pm), mu = mn == -INFINITY ? 0.f : mn;
-      const float al = exp2_f((M - mu) * c), be = exp2_f((pm - mu) * c);
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        o[i] = o[i] * al + be * *reinterpret_cast<const f32x4*>(part + (int64_t)r * D + 64 * i + 4 * lane);
-      l = l * al + be * pl;
-      M = mn;
-    }
-    const int64_t tok = row / G, out = (row0 + tok) * a.num_q_heads + cut.h * G + row - tok * G;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int r = r0 + threadIdx.x / 16;
+  const int64_t row = (int64_t)cut.tile * rows + r;
+  if (row >= all) return;
+  f32x4 o[E] = {};
+  float M = -INFINITY, l = 0.f;
+  for (int64_t v = w; v <= last; ++v) {
+    const float* part = parts + part_of(v, cut.at, per) * size;
+    const float pm = part[(int64_t)rows * D + 2 * r], pl = part[(int64_t)rows * D + 2 * r + 1];
+    const float mn = fmaxf(M, pm), mu = mn == -INFINITY ? 0.f : mn;
+    const float al = exp2_f((M - mu) * c), be = exp2_f((pm - mu) * c);
 #pragma unroll
     for (int i = 0; i < E; ++i)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) ((MT*)a.o)[out * D + 64 * i + 4 * lane + x] = from_f32<MT>(o[i][x] * inv);
-    if (a.lse && lane == 0) a.lse[out] = M * a.scale + (l == 0.f ? 0.f : logf(l));
+      o[i] = o[i] * al + be * *reinterpret_cast<const f32x4*>(part + (int64_t)r * D + 64 * i + 4 * lane);
+    l = l * al + be * pl;
+    M = mn;
   }
+  const int64_t tok = row / G, out = (row0 + tok) * a.num_q_heads + cut.h * G + row - tok * G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) ((MT*)a.o)[out * D + 64 * i + 4 * lane + x] = from_f32<MT>(o[i][x] * inv);
+  if (a.lse && lane == 0) a.lse[out] = M * a.scale + (l == 0.f ? 0.f : logf(l));
 }
 
 // Which kernel takes which sequence. Without cu_seqlens every sequence has the same rows; with
@@ -467,11 +447,11 @@ void launch_rows(const AttnArgs& a, bool rows) {
   if (tiles) launch_attn_tile(a, !rows);
   typedef TileShape<D, sizeof(MT) == 2> S;
   const int row_groups = rows ? kGroups : 0;
-  join_kernel<MT, D><<<row_groups + (tiles ? S::GROUPS * (S::ROWS / 64) : 0), kThreads, 0, a.stream>>>(a, row_groups);
+  join_kernel<MT, D><<<row_groups + (tiles ? S::GROUPS * (S::ROWS / 16) : 0), kThreads, 0, a.stream>>>(a, row_groups);
 }
 
 size_t row_bytes(int head_dim) {
-  return (256 + sizeof(Cut) * kGroups + (size_t)2 * kGroups * part_floats(head_dim) * 4 + 255) / 256 * 256;
+  return (sizeof(Cut) * kGroups + (size_t)2 * kGroups * part_floats(head_dim) * 4 + 255) / 256 * 256;
 }
 
 }  // namespace

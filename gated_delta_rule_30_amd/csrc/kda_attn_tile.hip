@@ -41,7 +41,7 @@ struct Tile {
 
 // The parts of a row are permuted in LDS so that what is read at once lies in different banks
 // (64 of 4 bytes): a key fragment is the same part of 16 rows, a transposed value fragment four parts of four
-// rows (fp32: 32 channels of two rows).
+// rows (fp32: consecutive parts of a row, left in place).
 template <typename MT, int D>
 __device__ __forceinline__ int k_at(int row, int part) {
   constexpr int RC = D * (int)sizeof(MT) / 16;
@@ -50,7 +50,7 @@ __device__ __forceinline__ int k_at(int row, int part) {
 template <typename MT, int D>
 __device__ __forceinline__ int v_at(int row, int part) {
   constexpr int RC = D * (int)sizeof(MT) / 16;
-  const int sw = sizeof(MT) == 4 ? ((row >> 2) & 1) << 3 : RC >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+  const int sw = sizeof(MT) == 4 ? 0 : RC >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
   return row * (RC * 16) + (part ^ sw) * 16;
 }
 
@@ -87,6 +87,7 @@ template <> struct Op<float> {
   }
   __device__ __forceinline__ static weights pack(const f32x16& s) { return {s}; }
   static constexpr int NF = 16;
+  static constexpr int together(int D) { return D >= 128 ? 4 : 2; }  // output tiles whose values lie side by side
   __device__ __forceinline__ static void hold(weights& w) { asm volatile("" : "+v"(w.f)); }
   __device__ __forceinline__ static f32x16 value(float v, const weights& w, int i, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x2f32(v, w.f[i], c, 0, 0, 0);
@@ -102,20 +103,37 @@ __device__ __forceinline__ bf16x8 value_frag(const char* v, int lane, int i, int
   const bf16x4 hi = ds_read_tr4((const bf16*)(v + v_at<bf16, D>(row + 8, part) + 8 * (lane & 1)));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-template <int D>
-__device__ __forceinline__ float value_frag(const char* v, int lane, int i, int c, float) {
-  const int h = lane >> 5, m = lane & 31;
-  return *(const lds_float*)(v + v_at<float, D>(8 * (i / 4) + 4 * h + i % 4, 8 * c + (m >> 2)) + 4 * (m & 3));
-}
-
 // O^T += V^T P^T
 template <typename MT, int D>
 __device__ __forceinline__ void add_values(const char* v, int lane, const typename Op<MT>::weights& p,
                                            f32x16 (&acc)[D / 32]) {
+  if constexpr (sizeof(MT) == 2) {
 #pragma unroll
-  for (int i = 0; i < Op<MT>::NF; ++i)
+    for (int i = 0; i < Op<MT>::NF; ++i)
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[c] = Op<MT>::value(value_frag<D>(v, lane, i, c, MT()), p, i, acc[c]);
+      for (int c = 0; c < D / 32; ++c) acc[c] = Op<MT>::value(value_frag<D>(v, lane, i, c, MT()), p, i, acc[c]);
+  } else {
+    // One product takes one float per lane, of one key and channel: the channels of V of tile c are so
+    // chosen (channel_of) that a lane reads those of all tiles of a key at once.
+    constexpr int W = Op<float>::together(D);
+    typedef __attribute__((ext_vector_type(W), may_alias)) float vec;
+    const int h = lane >> 5, m = lane & 31;
+#pragma unroll
+    for (int i = 0; i < Op<MT>::NF; ++i)
+#pragma unroll
+      for (int g = 0; g < D / 32 / W; ++g) {
+        const vec f = *(const vec*)(v + (8 * (i / 4) + 4 * h + i % 4) * (D * 4) + (32 * g + m) * (W * 4));
+#pragma unroll
+        for (int x = 0; x < W; ++x) acc[W * g + x] = Op<MT>::value(f[x], p, i, acc[W * g + x]);
+      }
+  }
+}
+// Channel of row `row` of output tile c.
+template <typename MT, int D>
+__device__ __forceinline__ int channel_of(int c, int row) {
+  if constexpr (sizeof(MT) == 2) return 32 * c + row;
+  constexpr int W = Op<float>::together(D);
+  return W * (32 * (c / W) + row) + c % W;
 }
 
 __global__ __launch_bounds__(kPlanThreads) void tile_plan_kernel(AttnArgs a) {
@@ -127,7 +145,7 @@ __global__ __launch_bounds__(kPlanThreads) void tile_plan_kernel(AttnArgs a) {
 // Where a workgroup is in its share: kept in LDS between tiles, and the arguments read again
 // where they are needed, so that the steps' loop holds no scalar registers that it does not use.
 struct Walk {
-  int64_t at, end, begin, t0, nt;  // units; the sequence's tiles t0 .. t0 + nt - 1
+  int64_t at, end, per, t0, nt;  // units; the sequence's tiles t0 .. t0 + nt - 1
   int n, h, tile, off;             // off: units of the tile that are done
 };
 __device__ __forceinline__ AttnArgs fresh_args() {
@@ -201,7 +219,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const int h = (int)((at - Hk * u0) / per_head);
     const int64_t off = at - Hk * u0 - h * per_head;
     const int tile = count(nt, [&](int64_t i) { return pl.pre[t0 + i + 1] - u0; }, off);
-    if (tid == 0) walk = {at, min(total, at + per), at, t0, nt, n, h, tile, (int)(off - (pl.pre[t0 + tile] - u0))};
+    if (tid == 0) walk = {at, min(total, at + per), per, t0, nt, n, h, tile, (int)(off - (pl.pre[t0 + tile] - u0))};
   }
   for (;;) {
     __syncthreads();  // `walk` is up to date, and LDS free of the last tile's use
@@ -231,9 +249,9 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const int nb = min(tk.units - off, left);  // steps
 
     // --- the wave's rows: lane m's query and its visible keys vlo .. vlo + span; and the steps full_lo ..
-    // full_lo + full_n - 1 that every row of the wave sees whole
+    // full_lo + full_n - 1 that every row of the wave sees whole, and those (some) that some row sees a part of
     const int key0 = tk.lo + off * SUB, hi_key = own(min(s.hi, key0 + nb * SUB));
-    int vlo, span, full_lo, full_n;
+    int vlo, span, full_lo, full_n, some_lo, some_n;
     v4u32 qf[SF];
     {
       const int row = tile * ROWS + wave * 32 + m;
@@ -245,12 +263,17 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       for (int i = 0; i < SF; ++i) qf[i] = *reinterpret_cast<const v4u32*>(src + 32 * i);
       vlo = phi >= plo ? plo : INT32_MAX;  // (nothing: no key is at or above that)
       span = max(0, phi - plo);
-      int lo = has ? plo : 0, hi = has ? phi : INT32_MAX;
+      int lo = has ? plo : 0, hi = has ? phi : INT32_MAX, slo = phi >= plo ? plo : INT32_MAX, shi = phi >= plo ? phi : -1;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         lo = max(lo, __shfl_xor(lo, d));
         hi = min(hi, __shfl_xor(hi, d));
+        slo = min(slo, __shfl_xor(slo, d));
+        shi = max(shi, __shfl_xor(shi, d));
       }
+      slo = max(0, slo - key0) / SUB;
+      some_lo = own(slo);
+      some_n = own(shi >= key0 ? max(0, (shi - key0) / SUB + 1 - slo) : 0);
       lo = max(0, lo - key0 + SUB - 1) / SUB;
       hi = hi >= key0 ? (int)(((int64_t)hi - key0 + 1) / SUB) : 0;
       full_lo = own(lo);
@@ -429,7 +452,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         // all of the phase's fragments are on their way before its first product: waiting for each in
         // turn costs more than the products
         f32x16 st = {};
-        decltype(value_frag<D>(vl, lane, 0, 0, MT())) vfr[Op<MT>::NF][NC];
+        bf16x8 vfr[Op<MT>::NF][NC];
         v4u32 kfr[SF];
 #pragma unroll
         for (int f = 0; f < Op<MT>::NF; ++f)
@@ -480,13 +503,15 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         look_up(i + 1, xk, xv);
         fetch(kbase, xk, kf);
         fetch(vbase, xv, vf);
-        f32x16 st;
-        float al;
-        scores(slot, st);
-        if (masked(i, ok >> 2)) mask(i, ok >> 2, st);
-        softmax(st, p, al);
-        rescale(al);
-        add_values<MT, D>(vl + slot, lane, p, acc);
+        if ((unsigned)(i - some_lo) < (unsigned)some_n) {
+          f32x16 st;
+          float al;
+          scores(slot, st);
+          if (masked(i, ok >> 2)) mask(i, ok >> 2, st);
+          softmax(st, p, al);
+          rescale(al);
+          add_values<MT, D>(vl + slot, lane, p, acc);
+        }
         put_k(BYTES - slot, kf);
         put_v(BYTES - slot, vf);
         lds_barrier();
@@ -509,7 +534,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         const MT* v = (const MT*)a.v_pages + pg * a.v_page_stride + ((int64_t)walk.h * ps + key % ps) * D;
 #pragma unroll
         for (int y = 0; y < NC * 16; ++y) {
-          const float f = (float)v[32 * (y / 16) + 8 * (y / 4 % 4) + 4 * h2 + y % 4];
+          const float f = (float)v[channel_of<MT, D>(y / 16, 8 * (y / 4 % 4) + 4 * h2 + y % 4)];
           if (f - f != 0.f) acc[y / 16][y % 16] += f;
         }
       }
@@ -530,25 +555,22 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
           const int tok = row / G;
           const int64_t out = (s.row0 + tok) * a.num_q_heads + h * G + row - tok * G;
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          MT* dst = (MT*)a.o + out * D + 4 * h2;
+          MT* dst = (MT*)a.o + out * D;
 #pragma unroll
           for (int x = 0; x < NC; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) dst[32 * x + 8 * y + e] = from_f32<MT>(acc[x][4 * y + e] * inv);
+            for (int y = 0; y < 16; ++y)
+              dst[channel_of<MT, D>(x, 8 * (y / 4) + 4 * h2 + y % 4)] = from_f32<MT>(acc[x][y] * inv);
           if (a.lse && h2 == 0) a.lse[out] = mx * a.scale + (l == 0.f ? 0.f : logf(l));
         } else {
           const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, ROWS));
-          const int64_t per = walk.end - walk.begin;  // (only the last share may be shorter, and nothing is cut at its end)
-          float* part = pl.part + part_of(share, walk.at, share ? walk.begin / share : per) * tile_part_floats(ROWS, D);
-          if (tid == 0 && off == 0) pl.cut[share] = {walk.at, n, h, tile, tk.units};
+          float* part = pl.part + part_of(share, walk.at, walk.per) * tile_part_floats(ROWS, D);
+          if (tid == 0 && off == 0) pl.cut[share] = {walk.at, walk.per, n, h, tile, tk.units};
 #pragma unroll
           for (int x = 0; x < NC; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              *reinterpret_cast<f32x4*>(part + (int64_t)r * D + 32 * x + 8 * y + 4 * h2) =
-                  f32x4{acc[x][4 * y], acc[x][4 * y + 1], acc[x][4 * y + 2], acc[x][4 * y + 3]};
+            for (int y = 0; y < 16; ++y)
+              part[(int64_t)r * D + channel_of<MT, D>(x, 8 * (y / 4) + 4 * h2 + y % 4)] = acc[x][y];
           if (h2 == 0) part[ROWS * D + 2 * r] = mx, part[ROWS * D + 2 * r + 1] = l;
         }
       }
