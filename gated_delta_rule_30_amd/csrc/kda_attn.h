@@ -135,11 +135,14 @@ __device__ __forceinline__ f32x4 odd_part(f32x4 x) {
 
 // ------------------------------------------------------------------ the tile kernel's plan
 // Sequences of more than row_limit rows go to the tile kernel (kda_attn_tile.hip), in tiles of
-// tile_rows rows. The plan numbers the tiles of all sequences, sequence n's from tile_first[n],
-// and adds up their units (32 keys): pre[i] are those of the tiles before tile i, for one K/V
-// head. All heads' units are laid end to end by (sequence, head, tile): sequence n starts at
-// Hk pre[tile_first[n]].
+// tile_rows rows. The plan numbers the tiles of all sequences, sequence n's from seq[n].tile,
+// and adds up what they cost for one K/V head: pre[i] is that of the tiles before tile i, seq[n].cost that of
+// the sequences before n. A tile costs its units (32 keys) and kTileLead more: what is done before its
+// first step and after its last takes about as long as that many steps (measured on a batch of short
+// sequences: 50 us without the lead, when one workgroup in a batch got many tiles of one unit). All
+// heads' tiles are laid end to end by (sequence, head, tile), each one's lead before its units.
 constexpr int kTileUnit = 32;
+constexpr int kTileLead = 4;
 
 // A workgroup's waves (of 32 rows each), the waves per SIMD that its registers allow,
 // and the workgroups: as many as the chip holds at once.
@@ -161,8 +164,12 @@ constexpr int attn_tile_groups(int D, bool bf16) {
   return attn_tile_shape(D, bf16, [](auto s) { return decltype(s)::GROUPS; });
 }
 
+struct SeqFirst {
+  int64_t tile, cost;
+};
 struct TilePlan {
-  int64_t *pre, *tile_first;
+  int64_t* pre;
+  SeqFirst* seq;
   Cut* cut;     // of each workgroup
   float* part;  // two partial results per workgroup: tile_rows rows of D sums, then m and l of each
 };
@@ -171,13 +178,13 @@ __host__ __device__ inline int64_t max_tiles(int num_seqs, int64_t total_tokens,
 }
 constexpr int kMaxTileGroups = 512;
 __host__ __device__ inline size_t tile_plan_bytes(int num_seqs, int64_t tiles) {
-  return (sizeof(Cut) * kMaxTileGroups + (size_t)(tiles + 1 + num_seqs + 1) * 8 + 255) / 256 * 256;
+  return (sizeof(Cut) * kMaxTileGroups + (size_t)(tiles + 1) * 8 + sizeof(SeqFirst) * (num_seqs + 1) + 255) / 256 * 256;
 }
 __host__ __device__ inline TilePlan tile_plan_at(char* ws, int num_seqs, int64_t tiles) {
   TilePlan p;
   p.cut = reinterpret_cast<Cut*>(ws);
-  p.tile_first = reinterpret_cast<int64_t*>(p.cut + kMaxTileGroups);
-  p.pre = p.tile_first + num_seqs + 1;
+  p.seq = reinterpret_cast<SeqFirst*>(p.cut + kMaxTileGroups);
+  p.pre = reinterpret_cast<int64_t*>(p.seq + num_seqs + 1);
   p.part = reinterpret_cast<float*>(ws + tile_plan_bytes(num_seqs, tiles));
   return p;
 }
@@ -236,10 +243,10 @@ __device__ __forceinline__ void make_tile_plan(const AttnArgs& a, PlanLds& lds) 
       if (s.rows > a.row_limit) tiles = (s.rows + a.tile_rows - 1) / a.tile_rows;
     }
     const int64_t x = carry + scan(tiles, &total);
-    if (n < N) pl.tile_first[n] = min(most, x - tiles);
+    if (n < N) pl.seq[n].tile = min(most, x - tiles);
     carry = min(most, carry + total);
   }
-  if (tid == 0) pl.tile_first[N] = carry;
+  if (tid == 0) pl.seq[N].tile = carry;
   __syncthreads();
   const int64_t tiles = carry;
   carry = 0;
@@ -250,16 +257,18 @@ __device__ __forceinline__ void make_tile_plan(const AttnArgs& a, PlanLds& lds) 
       int lo = 0, hi = N - 1;  // the last sequence that starts at or before tile i
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (pl.tile_first[mid] <= i) lo = mid;
+        if (pl.seq[mid].tile <= i) lo = mid;
         else hi = mid - 1;
       }
-      units = tile_keys(a, seq_at(a, lo, G, kTileUnit), (int)(i - pl.tile_first[lo]), G).units;
+      units = tile_keys(a, seq_at(a, lo, G, kTileUnit), (int)(i - pl.seq[lo].tile), G).units + kTileLead;
     }
     const int64_t x = carry + scan(units, &total);
     if (i < tiles) pl.pre[i] = x - units;
     carry += total;
   }
   if (tid == 0) pl.pre[tiles] = carry;
+  __syncthreads();
+  for (int n = tid; n <= N; n += kPlanThreads) pl.seq[n].cost = pl.pre[pl.seq[n].tile];
 }
 
 // plan: whether the plan has to be made first (else the row kernel's launch has made it)

@@ -145,8 +145,9 @@ __global__ __launch_bounds__(kPlanThreads) void tile_plan_kernel(AttnArgs a) {
 // Where a workgroup is in its share: kept in LDS between tiles, and the arguments read again
 // where they are needed, so that the steps' loop holds no scalar registers that it does not use.
 struct Walk {
-  int64_t at, end, per, t0, nt;  // units; the sequence's tiles t0 .. t0 + nt - 1
-  int n, h, tile, off;             // off: units of the tile that are done
+  int64_t at, end, per, t0, nt;  // (costs); the sequence's tiles are t0 .. t0 + nt - 1
+  int n, h, tile;
+  int64_t off;  // what of the tile, its lead first, is done
 };
 __device__ __forceinline__ AttnArgs fresh_args() {
   auto p = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
@@ -182,7 +183,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
   constexpr int RC = T::RC, NL = T::NL, SF = T::SF, NC = T::NC, ES = T::ES, BYTES = T::BYTES;
   constexpr bool TURNS = kWaves == 8;  // two waves per SIMD of this workgroup
   __shared__ __align__(16) char lds[T::LDS];
-  __shared__ int counts[kWaves];
+  __shared__ int any_odd;
   __shared__ Walk walk;
   char* const kl = lds;
   char* const vl = lds + 2 * BYTES;
@@ -196,30 +197,25 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const AttnArgs a = fresh_args();
     const int N = a.b.num_seqs, Hk = a.num_kv_heads, G = a.num_q_heads / Hk;
     const TilePlan pl = tile_plan_at(a.tile_ws, N, max_tiles(N, a.b.total_tokens, G, ROWS));
-    const int64_t total = Hk * pl.pre[pl.tile_first[N]], per = max((int64_t)1, (total + kGroups - 1) / kGroups);
+    const int64_t total = Hk * pl.seq[N].cost, per = max((int64_t)1, (total + kGroups - 1) / kGroups);
     const int64_t at = share * per;
     if (tid == 0) pl.cut[share].n = -1;
     if (at >= total) return;
-    // the entries of a sorted array that are at most x, counted over the threads
-    auto count = [&](int64_t n, auto entry, int64_t x) {
-      int c = 0;
-      for (int64_t i = tid; i < n; i += kThreads) c += entry(i) <= x;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d);
-      __syncthreads();
-      if (lane == 0) counts[wave] = c;
-      __syncthreads();
-      int all = 0;
-      for (int w = 0; w < kWaves; ++w) all += counts[w];
-      return all;
-    };
-    const int n = count(N, [&](int64_t i) { return Hk * pl.pre[pl.tile_first[i + 1]]; }, at);
-    const int64_t t0 = pl.tile_first[n], nt = pl.tile_first[n + 1] - t0, u0 = pl.pre[t0];
-    const int64_t per_head = pl.pre[t0 + nt] - u0;
-    const int h = (int)((at - Hk * u0) / per_head);
-    const int64_t off = at - Hk * u0 - h * per_head;
-    const int tile = count(nt, [&](int64_t i) { return pl.pre[t0 + i + 1] - u0; }, off);
-    if (tid == 0) walk = {at, min(total, at + per), per, t0, nt, n, h, tile, (int)(off - (pl.pre[t0 + tile] - u0))};
+    // the sequence that `at` lies in, and the tile: whichever thread has it tells the others
+    for (int n = tid; n < N; n += kThreads) {
+      const SeqFirst s = pl.seq[n], e = pl.seq[n + 1];
+      if (Hk * s.cost <= at && at < Hk * e.cost) {
+        const int64_t in = at - Hk * s.cost, per_head = e.cost - s.cost;
+        walk = {at, min(total, at + per), per, s.tile, e.tile - s.tile, n, (int)(in / per_head), 0, in % per_head};
+      }
+    }
+    __syncthreads();
+    const int64_t t0 = walk.t0, nt = walk.nt, u0 = pl.pre[t0], off = walk.off;
+    __syncthreads();
+    for (int64_t i = tid; i < nt; i += kThreads) {
+      const int64_t s = pl.pre[t0 + i] - u0, e = pl.pre[t0 + i + 1] - u0;
+      if (s <= off && off < e) walk.tile = (int)i, walk.off = off - s;
+    }
   }
   for (;;) {
     __syncthreads();  // `walk` is up to date, and LDS free of the last tile's use
@@ -233,15 +229,21 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
         walk.tile = 0;
         if (++walk.h == a.num_kv_heads) {
           walk.h = 0;
-          do ++walk.n, walk.t0 += walk.nt, walk.nt = pl.tile_first[walk.n + 1] - walk.t0;
+          do ++walk.n, walk.t0 += walk.nt, walk.nt = pl.seq[walk.n + 1].tile - walk.t0;
           while (walk.nt == 0);
         }
       }
       continue;
     }
+    if (walk.off < kTileLead) {
+      __syncthreads();
+      if (tid == 0) walk.at += kTileLead - walk.off, walk.off = kTileLead;
+      continue;
+    }
     const AttnArgs a = fresh_args();
     const int n = __builtin_amdgcn_readfirstlane(walk.n), h = __builtin_amdgcn_readfirstlane(walk.h),
-              tile = __builtin_amdgcn_readfirstlane(walk.tile), off = __builtin_amdgcn_readfirstlane(walk.off);
+              tile = __builtin_amdgcn_readfirstlane(walk.tile),
+              off = __builtin_amdgcn_readfirstlane((int)walk.off - kTileLead);
     const int left = __builtin_amdgcn_readfirstlane((int)min(walk.end - walk.at, (int64_t)INT32_MAX));
     const int G = a.num_q_heads / a.num_kv_heads;
     const Seq s = seq_at(a, n, G, SUB);
@@ -519,11 +521,11 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     }
 
     // --- the rows that see an infinity or NaN among the values gain it
-    if (tid == 0) counts[0] = 0;
+    if (tid == 0) any_odd = 0;
     __syncthreads();
-    if (odd_seen) counts[0] = 1;
+    if (odd_seen) any_odd = 1;
     __syncthreads();
-    if (counts[0]) {
+    if (any_odd) {
       const AttnArgs a = fresh_args();
       const int32_t* table = a.b.block_table + walk.n * a.b.table_stride;
       const int ps = a.b.page_size;
@@ -544,7 +546,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     {
       const AttnArgs a = fresh_args();
       const int N = a.b.num_seqs, G = a.num_q_heads / a.num_kv_heads;
-      const int n = walk.n, h = walk.h, tile = walk.tile, off = walk.off;
+      const int n = walk.n, h = walk.h, tile = walk.tile, off = (int)walk.off - kTileLead;
       const Seq s = seq_at(a, n, G, SUB);
       const TileKeys tk = tile_keys(a, s, tile, G);
       const bool done = off == 0 && nb == tk.units;
