@@ -5,6 +5,7 @@ marshalling only, as in _binding.py: every step runs in the library's HIP kernel
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -59,78 +60,85 @@ def _api():
 
 
 # ------------------------------------------------------------------ arguments
+# A decode step's calls take a few microseconds on the GPU, so what is checked here is checked
+# with few and cheap queries of each tensor.
 def _code(t, name):
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return KDA_DTYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return KDA_DTYPE_F32
     raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
 
 
-def _same(t, name, dtype, device):
+def _same(t, name, dtype, index):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, _device(index)))
+    if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
 
 
-def _array(t, name, dtype, device, shape):
-    _same(t, name, dtype, device)
-    if tuple(t.shape) != shape:
+def _device(index):
+    return torch.device("cuda", index) if index >= 0 else torch.device("cpu")
+
+
+def _array(t, name, dtype, index, shape):
+    _same(t, name, dtype, index)
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
 
-def _rows(t, name, dtype, device, rows, heads, dim):
+def _rows(t, name, dtype, index, rows, heads, dim):
     """Rows of contiguous heads [rows, heads, dim], any row stride; returns that stride."""
-    _same(t, name, dtype, device)
-    if tuple(t.shape) != (rows, heads, dim):
+    _same(t, name, dtype, index)
+    if t.shape != (rows, heads, dim):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, heads, dim)))
     s = t.stride()
-    if t.numel() and ((dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim)):
+    if ((s[2] != 1 and dim > 1) or (s[1] != dim and heads > 1)) and t.numel():
         raise ValueError("%s must have contiguous heads (only its rows may be strided)" % name)
     return s[0] if rows > 1 else heads * dim
 
 
-def _pages(t, name, dtype, device):
+def _pages(t, name, dtype, index):
     """Pages [P, heads, page_size, dim], contiguous each; returns the page stride."""
-    _same(t, name, dtype, device)
+    _same(t, name, dtype, index)
     if t.dim() != 4:
         raise ValueError("%s must be [pages, heads, page_size, dim], got shape %s"
                          % (name, tuple(t.shape)))
     P, H, ps, D = t.shape
     s = t.stride()
-    if (D > 1 and s[3] != 1) or s[2] != D or (H > 1 and s[1] != ps * D):
+    if (s[3] != 1 and D > 1) or s[2] != D or (s[1] != ps * D and H > 1):
         raise ValueError("%s must have contiguous pages (only the pages may be strided)" % name)
     return s[0] if P > 1 else H * ps * D
 
 
-def _table(t, device):
-    _same(t, "block_table", torch.int32, device)
+def _table(t, index):
+    _same(t, "block_table", torch.int32, index)
     if t.dim() != 2:
         raise ValueError("block_table must be [sequences, pages]")
     n, m = t.shape
-    if m > 1 and t.stride(1) != 1:
+    s = t.stride()
+    if s[1] != 1 and m > 1:
         raise ValueError("block_table must have contiguous rows")
-    return n, m, (t.stride(0) if n > 1 else m)
+    return n, m, (s[0] if n > 1 else m)
 
 
-def _cache(k_cache, v_cache, dtype, device):
-    ks, vs = _pages(k_cache, "k_cache", dtype, device), _pages(v_cache, "v_cache", dtype, device)
+def _cache(k_cache, v_cache, dtype, index):
+    ks, vs = _pages(k_cache, "k_cache", dtype, index), _pages(v_cache, "v_cache", dtype, index)
     if v_cache.shape != k_cache.shape:
         raise ValueError("v_cache has shape %s, expected %s" % (tuple(v_cache.shape),
                                                                tuple(k_cache.shape)))
     return ks, vs
 
 
-def _batch(block_table, seq_lens, cu_seqlens, device):
-    N, M, stride = _table(block_table, device)
-    _array(seq_lens, "seq_lens", torch.int32, device, (N,))
+def _batch(block_table, seq_lens, cu_seqlens, index):
+    N, M, stride = _table(block_table, index)
+    _array(seq_lens, "seq_lens", torch.int32, index, (N,))
     if cu_seqlens is not None:
-        _array(cu_seqlens, "cu_seqlens", torch.int32, device, (N + 1,))
+        _array(cu_seqlens, "cu_seqlens", torch.int32, index, (N + 1,))
     return N, M, stride
 
 
@@ -138,39 +146,40 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-class _on:
-    """The device of the tensors made current for a call, and that device's current stream."""
-
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError("tensors are on %s: the operators run on a GPU" % device)
-        self.index = device.index
-        self.guard = None
-
-    def __enter__(self):
-        if self.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _check(st, what):
+def _call(name, index, *args):
+    """The entry point ``name``, with the current stream of the tensors' device as its last argument and
+    that device current."""
+    if index < 0:
+        raise ValueError("%s runs on a GPU, its tensors are on the CPU" % name)
+    f = getattr(_READY or _api(), name)
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
-        raise KdaError(st, what)
+        raise KdaError(st, name)
 
 
-def _workspace(given, need, device, what):
+def _workspace(given, need, like, what):
     if need == 0:
         raise KdaError(1, what)
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
-    if given.device != device or not given.is_contiguous():
-        raise ValueError("workspace must be a contiguous buffer on %s" % device)
+        return like.new_empty(need, dtype=torch.uint8), need
+    if given.get_device() != like.get_device() or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous buffer on %s" % like.device)
     return given, given.numel() * given.element_size()
+
+
+# workspace sizes, functions of the arguments alone
+@functools.lru_cache(maxsize=256)
+def _attn_bytes(N, T, Hq, Hk, D, code):
+    return int(_api().kda_attn_paged_workspace_size(N, T, Hq, Hk, D, code))
+
+
+@functools.lru_cache(maxsize=256)
+def _plan_bytes(count, N, P):
+    return int(_api().kda_pages_plan_workspace_size(count, N, P))
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -212,8 +221,8 @@ def rope_freqs(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=
     return f.to(device), scale
 
 
-def _inv_freq(inv_freq, device):
-    _same(inv_freq, "inv_freq", torch.float64, device)
+def _inv_freq(inv_freq, index):
+    _same(inv_freq, "inv_freq", torch.float64, index)
     if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous vector")
     return 2 * inv_freq.shape[0]
@@ -223,35 +232,36 @@ def _rope(q, k, positions, inv_freq, flags, scale, q_out, k_out):
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
-    device, dtype, code = x.device, x.dtype, _code(x, "q and k")
+    index, dtype, code = x.get_device(), x.dtype, _code(x, "q and k")
     if x.dim() != 3:
         raise ValueError("q and k must be [tokens, heads, dim], got shape %s" % (tuple(x.shape),))
-    T, D = x.shape[0], x.shape[2]
-    _array(positions, "positions", torch.int32, device, (T,))
-    R = _inv_freq(inv_freq, device)
-    strides, heads, outs = [0, 0], [0, 0], [None, None]
-    for j, (name, t, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
-        if t is None:
-            if out is not None:
-                raise ValueError("%s_out is given without %s" % (name, name))
-            continue
-        heads[j] = t.shape[1] if t.dim() == 3 else -1
-        strides[j] = _rows(t, name, dtype, device, T, heads[j], D)
-        if out is None:
-            out = torch.empty((T, heads[j], D), dtype=dtype, device=device)
-        elif out.data_ptr() == t.data_ptr():
-            if _rows(out, name + "_out", dtype, device, T, heads[j], D) != strides[j]:
-                raise ValueError("%s_out in place of %s must have its strides" % (name, name))
-        else:
-            _array(out, name + "_out", dtype, device, (T, heads[j], D))
-        outs[j] = out
-    if T == 0:
-        return outs[0], outs[1]
-    with _on(device) as stream:
-        _check(_api().kda_rope(_p(q), _p(k), _p(positions), _p(inv_freq), T, heads[0], heads[1], D, R,
-                               strides[0], strides[1], code, flags, scale, _p(outs[0]), _p(outs[1]),
-                               stream), "kda_rope")
-    return outs[0], outs[1]
+    T, _, D = x.shape
+    _array(positions, "positions", torch.int32, index, (T,))
+    R = _inv_freq(inv_freq, index)
+    Hq, qs, q_out = _turned(q, q_out, "q", dtype, index, T, D)
+    Hk, ks, k_out = _turned(k, k_out, "k", dtype, index, T, D)
+    if T:
+        _call("kda_rope", index, _p(q), _p(k), positions.data_ptr(), inv_freq.data_ptr(), T, Hq, Hk, D, R,
+              qs, ks, code, flags, scale, _p(q_out), _p(k_out))
+    return q_out, k_out
+
+
+def _turned(t, out, name, dtype, index, T, D):
+    """(heads, row stride, output) of q or k: the output given (t itself, or apart), or a new one."""
+    if t is None:
+        if out is not None:
+            raise ValueError("%s_out is given without %s" % (name, name))
+        return 0, 0, None
+    H = t.shape[1] if t.dim() == 3 else -1
+    stride = _rows(t, name, dtype, index, T, H, D)
+    if out is None:
+        out = t.new_empty((T, H, D))
+    elif out.data_ptr() == t.data_ptr():
+        if _rows(out, name + "_out", dtype, index, T, H, D) != stride:
+            raise ValueError("%s_out in place of %s must have its strides" % (name, name))
+    else:
+        _array(out, name + "_out", dtype, index, (T, H, D))
+    return H, stride, out
 
 
 def rope(q, k, positions, inv_freq, interleaved=False, scale=1.0, q_out=None, k_out=None):
@@ -277,48 +287,33 @@ def cache_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None,
     of k_cache, v_cache [P, Hk, page_size, D] that block_table [N, max_pages] names. With
     inv_freq, k is turned by its position on the way, and q [T, Hq, D] too: returns q_out (else
     None)."""
-    device, dtype, code = k.device, k.dtype, _code(k, "k")
+    index, dtype, code = k.get_device(), k.dtype, _code(k, "k")
     if k.dim() != 3:
         raise ValueError("k must be [tokens, heads, dim], got shape %s" % (tuple(k.shape),))
     T, Hk, D = k.shape
-    N, M, ts = _batch(block_table, seq_lens, cu_seqlens, device)
-    kps, vps = _cache(k_cache, v_cache, dtype, device)
-    if k_cache.shape[1] != Hk or k_cache.shape[3] != D:
+    N, M, ts = _batch(block_table, seq_lens, cu_seqlens, index)
+    kps, vps = _cache(k_cache, v_cache, dtype, index)
+    P, heads, ps, dim = k_cache.shape
+    if heads != Hk or dim != D:
         raise ValueError("k_cache has shape %s, expected [pages, %d, page_size, %d]"
                          % (tuple(k_cache.shape), Hk, D))
-    ks, vs = _rows(k, "k", dtype, device, T, Hk, D), _rows(v, "v", dtype, device, T, Hk, D)
-    R = _inv_freq(inv_freq, device) if inv_freq is not None else 0
-    Hq, qs = 0, 0
-    if q is not None:
-        if inv_freq is None:
-            raise ValueError("q is turned by inv_freq, which is not given")
-        Hq = q.shape[1] if q.dim() == 3 else -1
-        qs = _rows(q, "q", dtype, device, T, Hq, D)
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=device)
-        elif q_out.data_ptr() == q.data_ptr():
-            if _rows(q_out, "q_out", dtype, device, T, Hq, D) != qs:
-                raise ValueError("q_out in place of q must have its strides")
-        else:
-            _array(q_out, "q_out", dtype, device, (T, Hq, D))
-    elif q_out is not None:
-        raise ValueError("q_out is given without q")
-    if T == 0:
-        return q_out
-    with _on(device) as stream:
-        _check(_api().kda_cache_append(
-            _p(q), _p(k), _p(v), qs, ks, vs, _p(k_cache), _p(v_cache), kps, vps, _p(block_table), ts,
-            _p(seq_lens), _p(cu_seqlens), N, T, Hq, Hk, D, k_cache.shape[0], M, k_cache.shape[2],
-            code, _p(inv_freq), R, ROPE_INTERLEAVED if interleaved else 0, scale, _p(q_out), stream),
-            "kda_cache_append")
+    ks, vs = _rows(k, "k", dtype, index, T, Hk, D), _rows(v, "v", dtype, index, T, Hk, D)
+    R = _inv_freq(inv_freq, index) if inv_freq is not None else 0
+    if q is not None and inv_freq is None:
+        raise ValueError("q is turned by inv_freq, which is not given")
+    Hq, qs, q_out = _turned(q, q_out, "q", dtype, index, T, D)
+    if T:
+        _call("kda_cache_append", index, _p(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, k_cache.data_ptr(),
+              v_cache.data_ptr(), kps, vps, block_table.data_ptr(), ts, seq_lens.data_ptr(), _p(cu_seqlens),
+              N, T, Hq, Hk, D, P, M, ps, code, _p(inv_freq), R, ROPE_INTERLEAVED if interleaved else 0,
+              scale, _p(q_out))
     return q_out
 
 
 def attn_workspace_size(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim, dtype) -> int:
     """Workspace bytes of attn_paged for this shape."""
     code = KDA_DTYPE_BF16 if dtype == torch.bfloat16 else KDA_DTYPE_F32
-    return int(_api().kda_attn_paged_workspace_size(num_seqs, total_tokens, num_q_heads,
-                                                    num_kv_heads, head_dim, code))
+    return _attn_bytes(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim, code)
 
 
 def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, scale=None, window=0,
@@ -328,48 +323,46 @@ def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, scal
     cache_append). ``scale`` defaults to D^-1/2; ``window`` > 0 keeps the last ``window`` keys
     of each row. ``lse`` (fp32 [T, Hq]) receives the log of each row's sum of e^score. Returns
     o [T, Hq, D]; a row with no key is 0, its lse -inf."""
-    device, dtype, code = q.device, q.dtype, _code(q, "q")
+    index, dtype, code = q.get_device(), q.dtype, _code(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, dim], got shape %s" % (tuple(q.shape),))
     T, Hq, D = q.shape
-    N, M, ts = _batch(block_table, seq_lens, cu_seqlens, device)
-    kps, vps = _cache(k_cache, v_cache, dtype, device)
-    P, Hk, ps, _ = k_cache.shape
-    if k_cache.shape[3] != D:
-        raise ValueError("k_cache has head dim %d, expected %d" % (k_cache.shape[3], D))
-    qs = _rows(q, "q", dtype, device, T, Hq, D)
+    N, M, ts = _batch(block_table, seq_lens, cu_seqlens, index)
+    kps, vps = _cache(k_cache, v_cache, dtype, index)
+    P, Hk, ps, dim = k_cache.shape
+    if dim != D:
+        raise ValueError("k_cache has head dim %d, expected %d" % (dim, D))
+    qs = _rows(q, "q", dtype, index, T, Hq, D)
     if o is None:
-        o = torch.empty((T, Hq, D), dtype=dtype, device=device)
+        o = q.new_empty((T, Hq, D))
     else:
-        _array(o, "o", dtype, device, (T, Hq, D))
+        _array(o, "o", dtype, index, (T, Hq, D))
     if lse is not None:
-        _array(lse, "lse", torch.float32, device, (T, Hq))
+        _array(lse, "lse", torch.float32, index, (T, Hq))
     if T == 0:
         return o
-    lib = _api()
-    need = lib.kda_attn_paged_workspace_size(N, T, Hq, Hk, D, code)
+    need = _attn_bytes(N, T, Hq, Hk, D, code)
     if need == 0:
         raise KdaError(2 if D not in (64, 128, 256) else 1, "kda_attn_paged_workspace_size")
-    with _on(device) as stream:
-        workspace, size = _workspace(workspace, need, device, "kda_attn_paged")
-        _check(lib.kda_attn_paged(
-            _p(q), qs, _p(k_cache), _p(v_cache), kps, vps, _p(block_table), ts, _p(seq_lens),
-            _p(cu_seqlens), N, T, Hq, Hk, D, P, M, ps, code, D ** -0.5 if scale is None else scale,
-            window, _p(o), _p(lse), _p(workspace), size, stream), "kda_attn_paged")
+    workspace, size = _workspace(workspace, need, q, "kda_attn_paged")
+    _call("kda_attn_paged", index, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), kps, vps,
+          block_table.data_ptr(), ts, seq_lens.data_ptr(), _p(cu_seqlens), N, T, Hq, Hk, D, P, M, ps, code,
+          D ** -0.5 if scale is None else scale, window, o.data_ptr(), _p(lse), workspace.data_ptr(), size)
     return o
 
 
 # ------------------------------------------------------------------ pages
-def _pool(t, page_dim, device):
-    """A kda_page_pool of a tensor whose dimension page_dim counts the pages: what follows it is
-    one page, what precedes it the planes."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError("a pool must be a torch.Tensor on %s" % device)
-    if not 0 <= page_dim < t.dim():
-        raise ValueError("page_dim %d of a pool of %d dimensions" % (page_dim, t.dim()))
-    shape, strides, es = t.shape, t.stride(), t.element_size()
+@functools.lru_cache(maxsize=256)
+def _pool_layout(shape, strides, es, page_dim):
+    """(outer_stride, page_stride, page_bytes, outer, num_pages) of a tensor whose dimension page_dim
+    counts the pages: what follows it is one page, what precedes it the planes."""
+    dims = len(shape)
+    if not 0 <= page_dim < dims:
+        raise ValueError("page_dim %d of a pool of %d dimensions" % (page_dim, dims))
+    if 0 in shape:
+        raise ValueError("a pool is empty")
     width = 1
-    for j in range(t.dim() - 1, page_dim, -1):
+    for j in range(dims - 1, page_dim, -1):
         if shape[j] != 1 and strides[j] != width:
             raise ValueError("a pool's pages must be contiguous")
         width *= shape[j]
@@ -383,39 +376,49 @@ def _pool(t, page_dim, device):
             raise ValueError("the dimensions before a pool's pages must be evenly spaced")
         outer *= shape[j]
     P = shape[page_dim]
-    if t.numel() == 0:
-        raise ValueError("a pool is empty")
-    return _Pool(t.data_ptr(), step * es, strides[page_dim] * es if P > 1 else 0, width * es, outer, P)
+    return step * es, strides[page_dim] * es if P > 1 else 0, width * es, outer, P
 
 
-def _pools(pools, page_dim, device):
+def _pools(pools, page_dim, index):
     if pools is None:
         return None, 0
     if isinstance(pools, torch.Tensor):
         pools = (pools,)
     if len(pools) > MAX_POOLS:
         raise ValueError("at most %d pools in one call, got %d" % (MAX_POOLS, len(pools)))
-    return (_Pool * len(pools))(*(_pool(t, page_dim, device) for t in pools)), len(pools)
+    arr = (_Pool * len(pools))()
+    for x, t in zip(arr, pools):
+        if not isinstance(t, torch.Tensor) or t.get_device() != index:
+            raise ValueError("a pool must be a torch.Tensor on %s" % _device(index))
+        x.base = t.data_ptr()
+        x.outer_stride, x.page_stride, x.page_bytes, x.outer, x.num_pages = _pool_layout(
+            t.shape, t.stride(), t.element_size(), page_dim)
+    return arr, len(pools)
+
+
+def _count(t, name, index):
+    """Entries of a vector of sequences, pages or token counts."""
+    _same(t, name, torch.int32, index)
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous vector" % name)
+    return t.shape[0]
 
 
 def _state(page_refs, block_table, seq_lens):
-    device = page_refs.device
-    if page_refs.dim() != 1:
-        raise ValueError("page_refs must be a vector")
-    _array(page_refs, "page_refs", torch.int32, device, (page_refs.shape[0],))
-    N, M, ts = _table(block_table, device)
+    index = page_refs.get_device()
+    P = _count(page_refs, "page_refs", index)
+    N, M, ts = _table(block_table, index)
     if seq_lens is not None:
-        _array(seq_lens, "seq_lens", torch.int32, device, (N,))
-    return device, page_refs.shape[0], N, M, ts
+        _array(seq_lens, "seq_lens", torch.int32, index, (N,))
+    return index, P, N, M, ts
 
 
-def _plan(granted, count, workspace, N, P, device):
+def _plan(granted, count, workspace, N, P, index, like):
     if granted is None:
-        granted = torch.empty(count, dtype=torch.int32, device=device)
+        granted = like.new_empty(count)
     else:
-        _array(granted, "granted", torch.int32, device, (count,))
-    workspace, size = _workspace(workspace, _api().kda_pages_plan_workspace_size(count, N, P), device,
-                                 "kda_pages_plan_workspace_size")
+        _array(granted, "granted", torch.int32, index, (count,))
+    workspace, size = _workspace(workspace, _plan_bytes(count, N, P), like, "kda_pages_plan_workspace_size")
     return granted, workspace, size
 
 
@@ -425,18 +428,16 @@ def pages_alloc(page_refs, block_table, seq_lens, new_tokens, page_size, seqs=No
     sequence i), from the lowest free pages, in order. page_refs [P], block_table [N,
     max_pages] and seq_lens [N], all int32, change in place. Returns granted [count] int32: 1,
     or 0 where nothing was done."""
-    device, P, N, M, ts = _state(page_refs, block_table, seq_lens)
-    count = new_tokens.shape[0] if new_tokens.dim() == 1 else -1
-    _array(new_tokens, "new_tokens", torch.int32, device, (count,))
+    index, P, N, M, ts = _state(page_refs, block_table, seq_lens)
+    count = _count(new_tokens, "new_tokens", index)
     if seqs is not None:
-        _array(seqs, "seqs", torch.int32, device, (count,))
+        _array(seqs, "seqs", torch.int32, index, (count,))
     elif count != N:
         raise ValueError("new_tokens has %d values for %d sequences" % (count, N))
-    with _on(device) as stream:
-        granted, workspace, size = _plan(granted, count, workspace, N, P, device)
-        _check(_api().kda_pages_alloc(_p(page_refs), _p(block_table), ts, _p(seq_lens), _p(seqs),
-                                      _p(new_tokens), count, N, P, M, page_size, _p(granted),
-                                      _p(workspace), size, stream), "kda_pages_alloc")
+    granted, workspace, size = _plan(granted, count, workspace, N, P, index, new_tokens)
+    _call("kda_pages_alloc", index, page_refs.data_ptr(), block_table.data_ptr(), ts, seq_lens.data_ptr(),
+          _p(seqs), new_tokens.data_ptr(), count, N, P, M, page_size, granted.data_ptr(),
+          workspace.data_ptr(), size)
     return granted
 
 
@@ -446,28 +447,24 @@ def pages_fork(pools, page_refs, block_table, seq_lens, parents, children, page_
     shared, a page that is not full is copied to the lowest free one in every pool. ``pools``:
     a tensor whose dimension ``page_dim`` counts the pages, up to 8 of them, or None (the
     bookkeeping alone). Returns granted [count] int32."""
-    device, P, N, M, ts = _state(page_refs, block_table, seq_lens)
-    count = children.shape[0] if children.dim() == 1 else -1
-    _array(children, "children", torch.int32, device, (count,))
-    _array(parents, "parents", torch.int32, device, (count,))
-    arr, n = _pools(pools, page_dim, device)
-    with _on(device) as stream:
-        granted, workspace, size = _plan(granted, count, workspace, N, P, device)
-        _check(_api().kda_pages_fork(arr, n, _p(page_refs), _p(block_table), ts, _p(seq_lens),
-                                     _p(parents), _p(children), count, N, P, M, page_size,
-                                     _p(granted), _p(workspace), size, stream), "kda_pages_fork")
+    index, P, N, M, ts = _state(page_refs, block_table, seq_lens)
+    count = _count(children, "children", index)
+    _array(parents, "parents", torch.int32, index, (count,))
+    arr, n = _pools(pools, page_dim, index)
+    granted, workspace, size = _plan(granted, count, workspace, N, P, index, children)
+    _call("kda_pages_fork", index, arr, n, page_refs.data_ptr(), block_table.data_ptr(), ts,
+          seq_lens.data_ptr(), parents.data_ptr(), children.data_ptr(), count, N, P, M, page_size,
+          granted.data_ptr(), workspace.data_ptr(), size)
     return granted
 
 
 def pages_free(page_refs, block_table, seq_lens, seqs, page_size):
     """kda_pages_free: the sequences seqs [count] int32 become empty; every page they hold loses
     one reference."""
-    device, P, N, M, ts = _state(page_refs, block_table, seq_lens)
-    count = seqs.shape[0] if seqs.dim() == 1 else -1
-    _array(seqs, "seqs", torch.int32, device, (count,))
-    with _on(device) as stream:
-        _check(_api().kda_pages_free(_p(page_refs), _p(block_table), ts, _p(seq_lens), _p(seqs), count,
-                                     N, P, M, page_size, stream), "kda_pages_free")
+    index, P, N, M, ts = _state(page_refs, block_table, seq_lens)
+    count = _count(seqs, "seqs", index)
+    _call("kda_pages_free", index, page_refs.data_ptr(), block_table.data_ptr(), ts, seq_lens.data_ptr(),
+          seqs.data_ptr(), count, N, P, M, page_size)
 
 
 def pages_compact(pools, page_refs, block_table, page_dim=0, out_refs=None, out_table=None,
@@ -475,37 +472,35 @@ def pages_compact(pools, page_refs, block_table, page_dim=0, out_refs=None, out_
     """kda_pages_compact: the highest live page moves to the lowest free page until the live
     pages are the lowest ones, in every pool (as in pages_fork) and, unless out_refs /
     out_table are given, in page_refs and block_table themselves. Returns moved, int32 [1]."""
-    device, P, N, M, ts = _state(page_refs, block_table, None)
-    arr, n = _pools(pools, page_dim, device)
+    index, P, N, M, ts = _state(page_refs, block_table, None)
+    arr, n = _pools(pools, page_dim, index)
     if out_refs is None:
         out_refs = page_refs
     else:
-        _array(out_refs, "out_refs", torch.int32, device, (P,))
+        _array(out_refs, "out_refs", torch.int32, index, (P,))
+    No, Mo, ots = N, M, ts
     if out_table is None:
         out_table = block_table
-    No, Mo, ots = _table(out_table, device)
+    else:
+        No, Mo, ots = _table(out_table, index)
     if (No, Mo) != (N, M):
         raise ValueError("out_table has shape %s, expected %s" % ((No, Mo), (N, M)))
     if moved is None:
-        moved = torch.empty(1, dtype=torch.int32, device=device)
+        moved = page_refs.new_empty(1)
     else:
-        _array(moved, "moved", torch.int32, device, (1,))
-    with _on(device) as stream:
-        workspace, size = _workspace(workspace, _api().kda_pages_compact_workspace_size(P), device,
-                                     "kda_pages_compact_workspace_size")
-        _check(_api().kda_pages_compact(arr, n, _p(page_refs), _p(block_table), ts, N, P, M,
-                                        _p(out_refs), _p(out_table), ots, _p(moved), _p(workspace),
-                                        size, stream), "kda_pages_compact")
+        _array(moved, "moved", torch.int32, index, (1,))
+    workspace, size = _workspace(workspace, _api().kda_pages_compact_workspace_size(P), page_refs,
+                                 "kda_pages_compact_workspace_size")
+    _call("kda_pages_compact", index, arr, n, page_refs.data_ptr(), block_table.data_ptr(), ts, N, P, M,
+          out_refs.data_ptr(), out_table.data_ptr(), ots, moved.data_ptr(), workspace.data_ptr(), size)
     return moved
 
 
 def pages_copy(pools, src, dst, page_dim=0):
     """kda_pages_copy: page src[i] to page dst[i] of every pool (any per-slot data: pages of a
     cache, or the states of KDA layers). No page may be a dst twice, or both a src and a dst."""
-    device = src.device
-    count = src.shape[0] if src.dim() == 1 else -1
-    _array(src, "src", torch.int32, device, (count,))
-    _array(dst, "dst", torch.int32, device, (count,))
-    arr, n = _pools(pools, page_dim, device)
-    with _on(device) as stream:
-        _check(_api().kda_pages_copy(arr, n, _p(src), _p(dst), count, stream), "kda_pages_copy")
+    index = src.get_device()
+    count = _count(src, "src", index)
+    _array(dst, "dst", torch.int32, index, (count,))
+    arr, n = _pools(pools, page_dim, index)
+    _call("kda_pages_copy", index, arr, n, src.data_ptr(), dst.data_ptr(), count)

@@ -461,8 +461,10 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
 #pragma unroll
           for (int x = 0; x < NC; ++x) vfr[f][x] = value_frag<D>(vl + (1 - odd) * BYTES, lane, f, x, MT());
 #pragma unroll
-        for (int f = 0; f < SF; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + odd * BYTES + k_at<MT, D>(m, 2 * f + h2));
+        for (int f = 0; f < SF / 2; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + odd * BYTES + k_at<MT, D>(m, 2 * f + h2));
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = SF / 2; f < SF; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + odd * BYTES + k_at<MT, D>(m, 2 * f + h2));
 #pragma unroll
         for (int f = 0; f < Op<MT>::NF; ++f)
 #pragma unroll
