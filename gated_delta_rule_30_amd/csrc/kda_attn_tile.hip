@@ -149,6 +149,11 @@ struct Walk {
   int n, h, tile;
   int64_t off;  // what of the tile, its lead first, is done
 };
+// The keys that some row of the tile sees, and the first and last step that has an infinity or NaN among
+// their values.
+struct Odd {
+  int seen_lo, seen_hi, first, last;
+};
 __device__ __forceinline__ AttnArgs fresh_args() {
   auto p = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(p));
@@ -183,7 +188,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
   constexpr int RC = T::RC, NL = T::NL, SF = T::SF, NC = T::NC, ES = T::ES, BYTES = T::BYTES;
   constexpr bool TURNS = kWaves == 8;  // two waves per SIMD of this workgroup
   __shared__ __align__(16) char lds[T::LDS];
-  __shared__ int any_odd;
+  __shared__ Odd odd;
   __shared__ Walk walk;
   char* const kl = lds;
   char* const vl = lds + 2 * BYTES;
@@ -250,6 +255,11 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     const TileKeys tk = tile_keys(a, s, tile, G);
     const int nb = min(tk.units - off, left);  // steps
 
+    if (tid == 0) {  // (read behind the next barrier, and last read before the one above)
+      const int last = (int)((min((int64_t)(tile + 1) * ROWS, (int64_t)s.rows) - 1) / G);
+      const int pf = s.p0 + (int)((int64_t)tile * ROWS / G);
+      odd = {a.window ? max(0, pf - a.window + 1) : 0, min(s.p0 + last, s.hi - 1), INT32_MAX, -1};
+    }
     // --- the wave's rows: lane m's query and its visible keys vlo .. vlo + span; and the steps full_lo ..
     // full_lo + full_n - 1 that every row of the wave sees whole, and those (some) that some row sees a part of
     const int key0 = tk.lo + off * SUB, hi_key = own(min(s.hi, key0 + nb * SUB));
@@ -283,7 +293,7 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     }
     const char* const kbase = own(a.k_pages + (int64_t)h * a.b.page_size * D * ES);
     const char* const vbase = own(a.v_pages + (int64_t)h * a.b.page_size * D * ES);
-    const float c = own(a.scale * LOG2E), slack = 8.f / c;
+    const float c = own(a.scale * LOG2E), slack = fminf(8.f / c, 1e30f);  // (finite: -inf + slack is -inf)
 
     // --- staging: a step's keys and values, thread by thread in 16-byte parts. A wave's parts lie in
     // one 16-key group of the step, or (GRPS 2) half of them in each; a group lies in one page.
@@ -351,17 +361,20 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       }
     };
     // An infinity or NaN is put as 0: it may lie where some row does not look, and a weight of 0 would not hide it.
-    // Rows that do see one get it at the end.
-    bool odd_seen = false;
-    auto put_v = [&](int slot, v4u32 (&r)[NL]) __attribute__((always_inline)) {
+    // If some row does see its key, the step is noted, and those rows get it at the end.
+    auto put_v = [&](int i, unsigned ok, int slot, v4u32 (&r)[NL]) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
         if (T::PARTS < kThreads && wave * 64 >= T::PARTS) break;
-        if (__any(any_nonfinite<MT>(r[j]))) {
-          r[j] = finite_part<MT>(r[j]);
-          odd_seen = true;
-        }
         const int x = j * kThreads + tid;
+        if (__any(any_nonfinite<MT>(r[j]))) {
+          const int key = key0 + i * SUB + x / RC;
+          if (any_nonfinite<MT>(r[j]) && key >= odd.seen_lo && key <= odd.seen_hi && (ok >> (x / RC / 16) & 1)) {
+            atomicMin(&odd.first, i);
+            atomicMax(&odd.last, i);
+          }
+          r[j] = finite_part<MT>(r[j]);
+        }
         *reinterpret_cast<v4u32*>(vl + slot + v_at<MT, D>(x / RC, x % RC)) = r[j];
       }
     };
@@ -441,13 +454,13 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       if (second) lds_barrier();
       // ODD: i & 1
       auto step = [&](int i, auto ODD, v4u32 (&kf)[NL], v4u32 (&vf)[NL]) __attribute__((always_inline)) {
-        constexpr int odd = decltype(ODD)::value;
+        constexpr int par = decltype(ODD)::value;
 #pragma unroll
         for (int g = 0; g < GRPS; ++g) yv[g] = xv[g];
         look_up(i + 3, xk, xv);  // `ok` ends at step i + 3 from here on
         auto put = [&]() __attribute__((always_inline)) {
-          put_k((1 - odd) * BYTES, kf);
-          put_v(odd * BYTES, vf);
+          put_k((1 - par) * BYTES, kf);
+          put_v(i, ok >> 6, par * BYTES, vf);
           fetch(kbase, xk, kf);
           fetch(vbase, yv, vf);
         };
@@ -459,12 +472,12 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
 #pragma unroll
         for (int f = 0; f < Op<MT>::NF; ++f)
 #pragma unroll
-          for (int x = 0; x < NC; ++x) vfr[f][x] = value_frag<D>(vl + (1 - odd) * BYTES, lane, f, x, MT());
+          for (int x = 0; x < NC; ++x) vfr[f][x] = value_frag<D>(vl + (1 - par) * BYTES, lane, f, x, MT());
 #pragma unroll
-        for (int f = 0; f < SF / 2; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + odd * BYTES + k_at<MT, D>(m, 2 * f + h2));
+        for (int f = 0; f < SF / 2; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + par * BYTES + k_at<MT, D>(m, 2 * f + h2));
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int f = SF / 2; f < SF; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + odd * BYTES + k_at<MT, D>(m, 2 * f + h2));
+        for (int f = SF / 2; f < SF; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + par * BYTES + k_at<MT, D>(m, 2 * f + h2));
 #pragma unroll
         for (int f = 0; f < Op<MT>::NF; ++f)
 #pragma unroll
@@ -499,7 +512,8 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       fetch(kbase, xk, kf);
       fetch(vbase, xv, vf);
       put_k(0, kf);
-      put_v(0, vf);
+      lds_barrier();
+      put_v(0, ok, 0, vf);
       lds_barrier();
 #pragma unroll 1
       for (int i = 0; i < nb; ++i) {
@@ -517,22 +531,18 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
           add_values<MT, D>(vl + slot, lane, p, acc);
         }
         put_k(BYTES - slot, kf);
-        put_v(BYTES - slot, vf);
+        put_v(i + 1, ok, BYTES - slot, vf);
         lds_barrier();
       }
     }
 
     // --- the rows that see an infinity or NaN among the values gain it
-    if (tid == 0) any_odd = 0;
-    __syncthreads();
-    if (odd_seen) any_odd = 1;
-    __syncthreads();
-    if (any_odd) {
+    if (odd.first <= odd.last) {
       const AttnArgs a = fresh_args();
       const int32_t* table = a.b.block_table + walk.n * a.b.table_stride;
-      const int ps = a.b.page_size;
+      const int ps = a.b.page_size, end = min(hi_key, key0 + (odd.last + 1) * SUB);
 #pragma unroll 1
-      for (int key = key0; key < hi_key; ++key) {
+      for (int key = key0 + odd.first * SUB; key < end; ++key) {
         const int pg = table[key / ps];
         if (!page_ok(pg, a.b.num_pages) || (unsigned)(key - vlo) > (unsigned)span) continue;
         const MT* v = (const MT*)a.v_pages + pg * a.v_page_stride + ((int64_t)walk.h * ps + key % ps) * D;

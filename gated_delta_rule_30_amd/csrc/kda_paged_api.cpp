@@ -212,7 +212,7 @@ static kda_status check_attn_shape(int32_t num_seqs, int64_t total_tokens, int32
                                    int32_t num_kv_heads, int32_t head_dim, kda_dtype dtype) {
   if (num_seqs <= 0 || num_seqs > kMaxSeqs || total_tokens < 0 || total_tokens > kMaxTokens ||
       !valid_heads(num_q_heads) || !valid_heads(num_kv_heads) || num_q_heads % num_kv_heads != 0 ||
-      total_tokens * num_q_heads > (int64_t)1 << 31)
+      total_tokens * num_q_heads > (int64_t)1 << 30)
     return KDA_ERROR_INVALID_VALUE;
   if (!valid_dtype(dtype) || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return KDA_ERROR_NOT_SUPPORTED;

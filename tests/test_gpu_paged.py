@@ -176,6 +176,35 @@ def test_values_alone_unseen(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_an_infinity_far_back(D, dtype):
+    """An infinity and a NaN among the values of a long context, in different parts of it: every row
+    that sees them carries them, in their channels alone."""
+    s = make([150, 1], [2500, 700], 4, 2, D, 32, dtype, seed=21)
+    o0, l0 = run(dev(s))
+    for n, j, ch, x in ((0, 1700, 3, -math.inf), (0, 77, D - 1, math.nan), (0, 2500 + 60, 17, math.inf), (1, 300, 9, math.inf)):
+        s["vc"][int(s["table"][n, j // 32]), 0, j % 32, ch] = x
+    o1, l1 = run(dev(s))
+    assert torch.equal(l0, l1) and torch.equal(o0[:, 2:], o1[:, 2:])
+    a, b = o1[:150, :2].float(), o1[150, :2].float()
+    assert (a[:, :, 3] == -math.inf).all() and torch.isnan(a[:, :, D - 1]).all()
+    assert (a[60:, :, 17] == math.inf).all() and torch.equal(o0[:60, :2, 17], o1[:60, :2, 17])
+    assert not torch.isfinite(b[:, 9]).any()
+    rest = [c for c in range(D) if c not in (3, 9, 17, D - 1)]
+    assert torch.equal(o0[:, :, rest], o1[:, :, rest])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [1e-36, 1e-3, 3.0])
+def test_scales(scale, dtype):
+    """From a scale that makes all weights equal to one that leaves a few: rows split over
+    workgroups and not."""
+    for new, ctx in (([1, 50], [1500, 100]), ([1, 1], [700, 20])):
+        s = make(new, ctx, 2, 1, 64, 16, dtype, seed=22)
+        check(s, *run(dev(s), scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_large_scores(dtype):
     """Scores of a few hundred, growing and falling along the sequence: the running maximum moves
     often, and early weights vanish."""
