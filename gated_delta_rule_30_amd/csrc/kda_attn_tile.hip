@@ -505,33 +505,35 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
     } else {
       // --- the steps, one wave per SIMD of this workgroup: step i's products and softmax in turn, the next step's
       // keys and values fetched meanwhile and put in LDS at the end
-      v4u32 kf[NL], vf[NL];
+      v4u32 staged[NL];
       int64_t xk[GRPS], xv[GRPS];
       read_table(0);
       look_up(0, xk, xv);
-      fetch(kbase, xk, kf);
-      fetch(vbase, xv, vf);
-      put_k(0, kf);
+      fetch(kbase, xk, staged);
+      put_k(0, staged);
+      fetch(vbase, xv, staged);
       lds_barrier();
-      put_v(0, ok, 0, vf);
+      put_v(0, ok, 0, staged);
       lds_barrier();
 #pragma unroll 1
       for (int i = 0; i < nb; ++i) {
         const int slot = (i & 1) * BYTES;
         look_up(i + 1, xk, xv);
-        fetch(kbase, xk, kf);
-        fetch(vbase, xv, vf);
-        if ((unsigned)(i - some_lo) < (unsigned)some_n) {
+        // one register set serves both: the keys come during the scores, the values during the output
+        fetch(kbase, xk, staged);
+        const bool some = (unsigned)(i - some_lo) < (unsigned)some_n;
+        if (some) {
           f32x16 st;
           float al;
           scores(slot, st);
           if (masked(i, ok >> 2)) mask(i, ok >> 2, st);
           softmax(st, p, al);
           rescale(al);
-          add_values<MT, D>(vl + slot, lane, p, acc);
         }
-        put_k(BYTES - slot, kf);
-        put_v(i + 1, ok, BYTES - slot, vf);
+        put_k(BYTES - slot, staged);
+        fetch(vbase, xv, staged);
+        if (some) add_values<MT, D>(vl + slot, lane, p, acc);
+        put_v(i + 1, ok, BYTES - slot, staged);
         lds_barrier();
       }
     }
