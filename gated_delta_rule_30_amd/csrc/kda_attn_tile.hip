@@ -450,57 +450,63 @@ __global__ __launch_bounds__((Tile<MT, D>::THREADS), (Tile<MT, D>::S::PER_SIMD))
       // "step -1", whose weights are 0
       for (int x = tid; x < T::PARTS; x += kThreads) *reinterpret_cast<v4u32*>(vl + BYTES + x * 16) = v4u32{0, 0, 0, 0};
       lds_barrier();
-      const bool second = wave >= kWaves / 2;
-      if (second) lds_barrier();
-      // ODD: i & 1
-      auto step = [&](int i, auto ODD, v4u32 (&kf)[NL], v4u32 (&vf)[NL]) __attribute__((always_inline)) {
-        constexpr int par = decltype(ODD)::value;
-#pragma unroll
-        for (int g = 0; g < GRPS; ++g) yv[g] = xv[g];
-        look_up(i + 3, xk, xv);  // `ok` ends at step i + 3 from here on
-        auto put = [&]() __attribute__((always_inline)) {
-          put_k((1 - par) * BYTES, kf);
-          put_v(i, ok >> 6, par * BYTES, vf);
-          fetch(kbase, xk, kf);
-          fetch(vbase, yv, vf);
+      // (each role has a loop of its own: in a shared one, where both could put, the compiler would wait for the
+      // loads just made)
+      auto run = [&](auto SECOND) __attribute__((always_inline)) {
+        constexpr bool second = decltype(SECOND)::value;
+        if constexpr (second) lds_barrier();
+        // ODD: i & 1
+        auto step = [&](int i, auto ODD, v4u32 (&kf)[NL], v4u32 (&vf)[NL]) __attribute__((always_inline)) {
+          constexpr int par = decltype(ODD)::value;
+  #pragma unroll
+          for (int g = 0; g < GRPS; ++g) yv[g] = xv[g];
+          look_up(i + 3, xk, xv);  // `ok` ends at step i + 3 from here on
+          auto put = [&]() __attribute__((always_inline)) {
+            put_k((1 - par) * BYTES, kf);
+            put_v(i, ok >> 6, par * BYTES, vf);
+            fetch(kbase, xk, kf);
+            fetch(vbase, yv, vf);
+          };
+          // all of the phase's fragments are on their way before its first product: waiting for each in
+          // turn costs more than the products
+          f32x16 st = {};
+          bf16x8 vfr[Op<MT>::NF][NC];
+          v4u32 kfr[SF];
+  #pragma unroll
+          for (int f = 0; f < Op<MT>::NF; ++f)
+  #pragma unroll
+            for (int x = 0; x < NC; ++x) vfr[f][x] = value_frag<D>(vl + (1 - par) * BYTES, lane, f, x, MT());
+  #pragma unroll
+          for (int f = 0; f < SF / 2; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + par * BYTES + k_at<MT, D>(m, 2 * f + h2));
+          __builtin_amdgcn_sched_barrier(0);
+  #pragma unroll
+          for (int f = SF / 2; f < SF; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + par * BYTES + k_at<MT, D>(m, 2 * f + h2));
+  #pragma unroll
+          for (int f = 0; f < Op<MT>::NF; ++f)
+  #pragma unroll
+            for (int x = 0; x < NC; ++x) acc[x] = Op<MT>::value(vfr[f][x], p, f, acc[x]);
+  #pragma unroll
+          for (int f = 0; f < SF; ++f) st = Op<MT>::score(kfr[f], qf[f], st);
+          if constexpr (second) put();
+          lds_barrier();
+          if (masked(i, ok >> 6)) mask(i, ok >> 6, st);
+          float al;
+          softmax(st, p, al);
+          rescale(al);
+          if constexpr (!second) put();
+          lds_barrier();
         };
-        // all of the phase's fragments are on their way before its first product: waiting for each in
-        // turn costs more than the products
-        f32x16 st = {};
-        bf16x8 vfr[Op<MT>::NF][NC];
-        v4u32 kfr[SF];
-#pragma unroll
-        for (int f = 0; f < Op<MT>::NF; ++f)
-#pragma unroll
-          for (int x = 0; x < NC; ++x) vfr[f][x] = value_frag<D>(vl + (1 - par) * BYTES, lane, f, x, MT());
-#pragma unroll
-        for (int f = 0; f < SF / 2; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + par * BYTES + k_at<MT, D>(m, 2 * f + h2));
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int f = SF / 2; f < SF; ++f) kfr[f] = *reinterpret_cast<const v4u32*>(kl + par * BYTES + k_at<MT, D>(m, 2 * f + h2));
-#pragma unroll
-        for (int f = 0; f < Op<MT>::NF; ++f)
-#pragma unroll
-          for (int x = 0; x < NC; ++x) acc[x] = Op<MT>::value(vfr[f][x], p, f, acc[x]);
-#pragma unroll
-        for (int f = 0; f < SF; ++f) st = Op<MT>::score(kfr[f], qf[f], st);
-        if (second) put();
-        lds_barrier();
-        if (masked(i, ok >> 6)) mask(i, ok >> 6, st);
-        float al;
-        softmax(st, p, al);
-        rescale(al);
-        if (!second) put();
-        lds_barrier();
+        int i = 0;
+  #pragma unroll 1
+        for (; i + 1 < nb; i += 2) {
+          step(i, std::integral_constant<int, 0>(), k0, v0);
+          step(i + 1, std::integral_constant<int, 1>(), k1, v1);
+        }
+        if (i < nb) step(i, std::integral_constant<int, 0>(), k0, v0);
+        if constexpr (!second) lds_barrier();
       };
-      int i = 0;
-#pragma unroll 1
-      for (; i + 1 < nb; i += 2) {
-        step(i, std::integral_constant<int, 0>(), k0, v0);
-        step(i + 1, std::integral_constant<int, 1>(), k1, v1);
-      }
-      if (i < nb) step(i, std::integral_constant<int, 0>(), k0, v0);
-      if (!second) lds_barrier();
+      if (wave >= kWaves / 2) run(std::true_type());
+      else run(std::false_type());
       add_values<MT, D>(vl + ((nb - 1) & 1) * BYTES, lane, p, acc);
     } else {
       // --- the steps, one wave per SIMD of this workgroup: step i's products and softmax in turn, the next step's
