@@ -2,19 +2,27 @@
 // (kda_attn.hip takes the sequences of few rows).
 //
 // The formulas and the one pass with a running maximum are those of kda_attn.hip. Bound by the
-// matrix cores: 4 D flops per (row, key). A workgroup of four waves takes a tile of 256 (or 128)
-// rows of one sequence and K/V head, each wave 64 (32) of them, and walks over the keys 32 at a
-// time, staged through LDS for all four.
+// matrix cores: 4 D flops per (row, key). A workgroup takes a tile of one sequence and K/V head, 32 rows
+// per wave (8 waves; fp32 and D = 256: 4, for whose registers there is no more room), and walks over the
+// keys 32 at a time, staged through LDS for all of its waves.
 //  - Scores are formed transposed, S^T = K Q^T, in 32 x 32 tiles: a lane holds 16 scores of one
 //    row, so that the softmax is register work and one lane exchange, and the weights are already laid
 //    out as the second operand of O^T = V^T P^T. The order of keys within an operand is free as long as
 //    both operands share it, so no weight moves between lanes.
-//  - 64 rows per wave halve the LDS reads per flop: with 32, four waves read 128 bytes per clock
-//    at the full matrix rate, all that LDS gives.
+//  - With 8 waves the two waves of a SIMD take turns, one in its products while the other is in its softmax. A
+//    step of a wave is 512 clocks of products and about 400 of vector work; left to themselves the waves
+//    drift into the same phase (the case below, when this was built: 1.69 ms without turns, 1.34 with).
+//  - Loads are made two steps ahead: a step takes 1.1 us, about as long as
+//    a key is on its way from HBM (one step ahead 1370 us, two 1285 to 1257).
 //  - The output is rescaled only when a maximum grows by more than 2^8: weights up to 2^8 cost
 //    neither the fp32 sums nor the bf16 weights any relative accuracy.
 //  - The tiles' keys are laid end to end and cut into equal shares, one per workgroup; a tile
 //    that is cut leaves partial (o, m, l), joined with those of the row kernel.
+// Measured: 4096 new tokens behind 16384, 32 query heads over 8, D = 128, bf16: 1257 us, 984 TFLOP/s
+// (a library product of 16384^3 bf16 reaches 1381 on the same card; the kernel with its loads of keys and
+// values taken out 1310, so what is left is mostly memory latency and a clock held down by power). fp32: 3
+// sequences, 432 new tokens over 5392, 16 heads: 106 us; 9.7 GFLOP with the rows that pad the last tiles, at 92 of
+// the 154 TFLOP/s of a library product.
 #include "kda_attn.h"
 
 namespace kda {

@@ -8,6 +8,8 @@
 // fp64 turns reduced to [-1/2, 1/2] (an fp32 product p f would be off by up to 2^-24 p f radians,
 // 0.06 at p f = 10^6), keeps them in LDS as fp32, and then streams the heads: one unit is 16 channels
 // (8 pairs) of one head, two 16-byte loads and stores in bf16.
+// Measured: 16384 tokens of 32 + 8 heads of 128, bf16: 336 MB in 54 us, 6.2 TB/s. The append of 20 chunks of 64 to
+// 2048 tokens (213 MB): 34 to 35 us, 6.2 TB/s; of 256 single tokens (6 MB): 4.5 us, launch and latency.
 #include "kda_device.h"
 #include "kda_paged_int.h"
 
