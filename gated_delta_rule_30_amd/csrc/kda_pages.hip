@@ -26,20 +26,21 @@ constexpr int kPart = 8192;    // bytes of a page that one workgroup copies at a
 __device__ __forceinline__ int pages_of(int64_t len, int ps) { return (int)((len + ps - 1) / ps); }
 
 // Inclusive prefix sum over the workgroup's threads, in thread order; *total gets the sum.
-__device__ __forceinline__ int block_scan(int x, int* lds, int* total) {
+template <typename X>
+__device__ __forceinline__ X block_scan(X x, X* lds, X* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
+    const X y = __shfl_up(x, d);
     if (lane >= d) x += y;
   }
   __syncthreads();  // lds may still be read by the previous call
   if (lane == 63) lds[wave] = x;
   __syncthreads();
-  int before = 0, all = 0;
+  X before = 0, all = 0;
   for (int w = 0; w < waves; ++w) {
-    const int s = lds[w];
-    before += w < wave ? s : 0;
+    const X s = lds[w];
+    before += w < wave ? s : X(0);
     all += s;
   }
   *total = all;
@@ -126,6 +127,7 @@ constexpr int kClaims = 8192;  // sequences whose claims fit in LDS
 template <bool FORK>
 __global__ __launch_bounds__(kPlan) void plan_kernel(PagesArgs a) {
   __shared__ int lds[kPlan / 64], claims[kClaims];
+  __shared__ int64_t sums[kPlan / 64];
   const Plan pl = plan_at(a.workspace, a.count, a.num_seqs);
   const int tid = threadIdx.x, ps = a.page_size;
   Refs refs = load_refs(a.page_refs, tid * 16, a.num_pages);  // on their way while the requests are looked at
@@ -166,8 +168,8 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(PagesArgs a) {
           need = pages_of(to, ps) - pages_of(len, ps);
       }
     }
-    int total;
-    const int incl = block_scan(max(need, 0), lds, &total);
+    int64_t total;  // (1024 needs of long rows pass 32 bits)
+    const int64_t incl = block_scan((int64_t)max(need, 0), sums, &total);
     if (i < a.count) {
       const int64_t r = carry + incl - max(need, 0);
       pl.rank[i] = (int)min(r, (int64_t)a.num_pages);  // past the last page: never granted

@@ -142,6 +142,17 @@ def test_many_requests():
     b.compact()
 
 
+def test_needs_past_32_bits():
+    """1024 requests of 2^21 pages each pass 32 bits together; none fits, and neither does what follows them."""
+    N, width, ps, P = 1026, 1 << 21, 16, 64
+    table = torch.empty((N, width), dtype=torch.int32, device=DEV)
+    refs, lens = ints([0] * P), ints([0] * N)
+    new = [width * ps] * 1024 + [1, 0]
+    got = kda.pages_alloc(refs, table, lens, ints(new), ps)
+    assert got.tolist() == [0] * 1025 + [1]
+    assert refs.tolist() == [0] * P and lens.tolist() == [0] * N
+
+
 def test_entries_outside_the_pool():
     """Entries that name no page are passed over by fork, free and compact."""
     b = Both(12, 4, 4, 16)
