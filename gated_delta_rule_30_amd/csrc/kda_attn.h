@@ -39,7 +39,8 @@ __device__ __forceinline__ Seq seq_at(const AttnArgs& a, int n, int G, int unit)
   const int64_t len = a.b.seq_lens[n], cap = (int64_t)a.b.max_pages * a.b.page_size;
   s.rows = (int)(m * G);
   s.p0 = (int)max(len - m, (int64_t)INT32_MIN);
-  s.hi = (int)max((int64_t)0, min(min(len, cap), (int64_t)INT32_MAX - 4096));
+  // (the kernels look a few thousand keys ahead of the last one, which 32 bits still have to hold)
+  s.hi = (int)max((int64_t)0, min(min(len, cap), (int64_t)INT32_MAX - 65535));
   const int64_t lo = a.window ? (int64_t)s.p0 - a.window + 1 : 0;
   s.lo = lo > 0 ? (int)(lo / unit) * unit : 0;
   if (m == 0 || s.lo >= s.hi) s.lo = s.hi = 0;

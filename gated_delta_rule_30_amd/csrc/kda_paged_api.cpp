@@ -11,6 +11,7 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int kMaxHeads = 4096;
 constexpr int kMaxSeqs = 1 << 20;
+constexpr int kMaxPages = 1 << 30;
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool valid_dtype(kda_dtype t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_BF16; }
@@ -28,6 +29,14 @@ int64_t extent(int64_t rows, int64_t width, int64_t stride, int64_t es) {
   return rows > 0 ? ((rows - 1) * stride + width) * es : 0;
 }
 
+// Whether rows a and b, of na and nb bytes, overlap; with one stride they may lie between each other.
+bool rows_overlap(const void* a, int64_t na, int64_t stride_a, const void* b, int64_t nb, int64_t stride_b, int64_t rows) {
+  if (!overlap(a, extent(rows, na, stride_a, 1), b, extent(rows, nb, stride_b, 1))) return false;
+  if (stride_a != stride_b || rows < 2) return true;
+  const int64_t d = reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a), in = (d % stride_a + stride_a) % stride_a;
+  return in < na || in + nb > stride_a;
+}
+
 // Rows of heads: 16-byte pointer and stride, rows that do not overlap.
 bool bad_rows(const void* p, int64_t stride, int64_t width, int64_t es) {
   return !p || !aligned(p, 16) || stride < width || stride > kMaxStride || stride * es % 16 != 0;
@@ -38,7 +47,8 @@ kda_status check_batch(const int32_t* block_table, int64_t table_stride, const i
                        const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens,
                        int32_t num_pages, int32_t max_pages, int32_t page_size) {
   if (num_seqs <= 0 || num_seqs > kMaxSeqs || total_tokens < 0 || total_tokens > kMaxTokens ||
-      num_pages <= 0 || max_pages <= 0 || table_stride < max_pages || table_stride > kMaxStride)
+      num_pages <= 0 || num_pages > kMaxPages || max_pages <= 0 || table_stride < max_pages ||
+      table_stride > kMaxStride)
     return KDA_ERROR_INVALID_VALUE;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
     return KDA_ERROR_NOT_SUPPORTED;
@@ -92,8 +102,8 @@ kda_status check_pools(const kda_page_pool* pools, int32_t num_pools, int32_t nu
 kda_status check_tables(const int32_t* page_refs, const int32_t* block_table, int64_t table_stride,
                         const int32_t* seq_lens, int32_t count, int32_t num_seqs,
                         int32_t num_pages, int32_t max_pages, int32_t page_size) {
-  if (count < 0 || count > kMaxSeqs || num_seqs <= 0 || num_seqs > kMaxSeqs || num_pages <= 0 || max_pages <= 0 ||
-      table_stride < max_pages || table_stride > kMaxStride)
+  if (count < 0 || count > kMaxSeqs || num_seqs <= 0 || num_seqs > kMaxSeqs || num_pages <= 0 ||
+      num_pages > kMaxPages || max_pages <= 0 || table_stride < max_pages || table_stride > kMaxStride)
     return KDA_ERROR_INVALID_VALUE;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
     return KDA_ERROR_NOT_SUPPORTED;
@@ -133,6 +143,9 @@ extern "C" kda_status kda_rope(const void* q, const void* k, const int32_t* posi
   if ((!q_in && (overlap(q_out, T * wq * es, q, qe) || overlap(q_out, T * wq * es, k, ke))) ||
       (!k_in && (overlap(k_out, T * wk * es, k, ke) || overlap(k_out, T * wk * es, q, qe))) ||
       (q && k && !q_in && !k_in && overlap(q_out, T * wq * es, k_out, T * wk * es)))
+    return KDA_ERROR_INVALID_VALUE;
+  // what is turned in place is not read as another's input
+  if (q && k && (q_in || k_in) && rows_overlap(q, wq * es, q_stride * es, k, wk * es, k_stride * es, T))
     return KDA_ERROR_INVALID_VALUE;
   if (q && q == k) return KDA_ERROR_INVALID_VALUE;
   kda::RopeArgs a = {};
@@ -185,6 +198,10 @@ extern "C" kda_status kda_cache_append(
     if (overlap(in[i], in_n[i], k_pages, kp) || overlap(in[i], in_n[i], v_pages, vp))
       return KDA_ERROR_INVALID_VALUE;
   if (k_pages == v_pages) return KDA_ERROR_INVALID_VALUE;
+  if (q && q_out == q &&
+      (rows_overlap(q, wq * es, q_stride * es, k, wk * es, k_stride * es, T) ||
+       rows_overlap(q, wq * es, q_stride * es, v, wk * es, v_stride * es, T)))
+    return KDA_ERROR_INVALID_VALUE;
   if (q && q_out != q) {
     const int64_t n = T * wq * es;
     if (overlap(q_out, n, q, qe) || overlap(q_out, n, k, ke) || overlap(q_out, n, v, ve) ||
@@ -256,9 +273,12 @@ extern "C" kda_status kda_attn_paged(const void* q, int64_t q_stride, const void
       overlap(lse, le, o, oe))
     return KDA_ERROR_INVALID_VALUE;
   if (!workspace || !aligned(workspace, 256)) return KDA_ERROR_INVALID_VALUE;
-  if (workspace_bytes < kda::attn_workspace_bytes(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim,
-                                                  dtype == KDA_DTYPE_BF16))
-    return KDA_ERROR_WORKSPACE_TOO_SMALL;
+  const int64_t need = (int64_t)kda::attn_workspace_bytes(num_seqs, total_tokens, num_q_heads, num_kv_heads, head_dim,
+                                                          dtype == KDA_DTYPE_BF16);
+  if (workspace_bytes < (size_t)need) return KDA_ERROR_WORKSPACE_TOO_SMALL;
+  if (overlap(workspace, need, q, qe) || overlap(workspace, need, o, oe) || overlap(workspace, need, lse, le) ||
+      overlap(workspace, need, k_pages, kp) || overlap(workspace, need, v_pages, vp))
+    return KDA_ERROR_INVALID_VALUE;
   kda::AttnArgs a = {};
   a.q = q, a.q_stride = q_stride;
   a.k_pages = static_cast<const char*>(k_pages), a.v_pages = static_cast<const char*>(v_pages);
@@ -275,16 +295,24 @@ extern "C" kda_status kda_attn_paged(const void* q, int64_t q_stride, const void
 }
 
 extern "C" size_t kda_pages_plan_workspace_size(int32_t count, int32_t num_seqs, int32_t num_pages) {
-  if (count < 0 || count > kMaxSeqs || num_seqs <= 0 || num_seqs > kMaxSeqs || num_pages <= 0) return 0;
+  if (count < 0 || count > kMaxSeqs || num_seqs <= 0 || num_seqs > kMaxSeqs || num_pages <= 0 || num_pages > kMaxPages)
+    return 0;
   return kda::pages_plan_bytes(count, num_seqs, num_pages);
 }
 
-static kda_status check_plan(int32_t count, int32_t num_seqs, int32_t num_pages,
-                             const int32_t* granted, const void* workspace, size_t workspace_bytes) {
-  if (!granted || !aligned(granted, 4) || !workspace || !aligned(workspace, 256))
+// granted and the workspace lie apart from each other and from the tables.
+static kda_status check_plan(const kda::PagesArgs& a, const void* workspace, size_t workspace_bytes) {
+  if (!a.granted || !aligned(a.granted, 4) || !workspace || !aligned(workspace, 256))
     return KDA_ERROR_INVALID_VALUE;
-  return workspace_bytes < kda::pages_plan_bytes(count, num_seqs, num_pages) ? KDA_ERROR_WORKSPACE_TOO_SMALL
-                                                                              : KDA_SUCCESS;
+  const int64_t need = (int64_t)kda::pages_plan_bytes(a.count, a.num_seqs, a.num_pages), ge = (int64_t)a.count * 4;
+  if (workspace_bytes < (size_t)need) return KDA_ERROR_WORKSPACE_TOO_SMALL;
+  const void* tables[] = {a.page_refs, a.block_table, a.seq_lens};
+  const int64_t bytes[] = {(int64_t)a.num_pages * 4, extent(a.num_seqs, a.max_pages, a.table_stride, 4),
+                           (int64_t)a.num_seqs * 4};
+  for (int i = 0; i < 3; ++i)
+    if (overlap(workspace, need, tables[i], bytes[i]) || overlap(a.granted, ge, tables[i], bytes[i]))
+      return KDA_ERROR_INVALID_VALUE;
+  return overlap(workspace, need, a.granted, ge) ? KDA_ERROR_INVALID_VALUE : KDA_SUCCESS;
 }
 
 extern "C" kda_status kda_pages_alloc(int32_t* page_refs, int32_t* block_table, int64_t table_stride,
@@ -299,8 +327,6 @@ extern "C" kda_status kda_pages_alloc(int32_t* page_refs, int32_t* block_table, 
   if (!seqs && count != num_seqs) return KDA_ERROR_INVALID_VALUE;
   if (count == 0) return KDA_SUCCESS;
   if (!new_tokens || !aligned(new_tokens, 4) || (seqs && !aligned(seqs, 4))) return KDA_ERROR_INVALID_VALUE;
-  st = check_plan(count, num_seqs, num_pages, granted, workspace, workspace_bytes);
-  if (st != KDA_SUCCESS) return st;
   kda::PagesArgs a = {};
   a.page_refs = page_refs, a.block_table = block_table, a.seq_lens = seq_lens;
   a.table_stride = table_stride;
@@ -308,6 +334,8 @@ extern "C" kda_status kda_pages_alloc(int32_t* page_refs, int32_t* block_table, 
   a.count = count, a.num_seqs = num_seqs, a.num_pages = num_pages, a.max_pages = max_pages;
   a.page_size = page_size;
   a.granted = granted;
+  st = check_plan(a, workspace, workspace_bytes);
+  if (st != KDA_SUCCESS) return st;
   a.workspace = static_cast<char*>(workspace);
   a.stream = static_cast<hipStream_t>(stream);
   return done(kda::launch_pages_alloc(a));
@@ -328,14 +356,14 @@ extern "C" kda_status kda_pages_fork(const kda_page_pool* pools, int32_t num_poo
   if (st != KDA_SUCCESS) return st;
   if (count == 0) return KDA_SUCCESS;
   if (!parents || !aligned(parents, 4) || !children || !aligned(children, 4)) return KDA_ERROR_INVALID_VALUE;
-  st = check_plan(count, num_seqs, num_pages, granted, workspace, workspace_bytes);
-  if (st != KDA_SUCCESS) return st;
   a.page_refs = page_refs, a.block_table = block_table, a.seq_lens = seq_lens;
   a.table_stride = table_stride;
   a.seqs = children, a.parents = parents;
   a.count = count, a.num_seqs = num_seqs, a.num_pages = num_pages, a.max_pages = max_pages;
   a.page_size = page_size;
   a.granted = granted;
+  st = check_plan(a, workspace, workspace_bytes);
+  if (st != KDA_SUCCESS) return st;
   a.workspace = static_cast<char*>(workspace);
   a.stream = static_cast<hipStream_t>(stream);
   return done(kda::launch_pages_fork(a));
@@ -361,7 +389,7 @@ extern "C" kda_status kda_pages_free(int32_t* page_refs, int32_t* block_table, i
 }
 
 extern "C" size_t kda_pages_compact_workspace_size(int32_t num_pages) {
-  return num_pages <= 0 ? 0 : kda::pages_compact_bytes(num_pages);
+  return num_pages <= 0 || num_pages > kMaxPages ? 0 : kda::pages_compact_bytes(num_pages);
 }
 
 extern "C" kda_status kda_pages_compact(const kda_page_pool* pools, int32_t num_pools,
@@ -390,7 +418,12 @@ extern "C" kda_status kda_pages_compact(const kda_page_pool* pools, int32_t num_
       overlap(moved, 4, out_table, oe))
     return KDA_ERROR_INVALID_VALUE;
   if (!workspace || !aligned(workspace, 256)) return KDA_ERROR_INVALID_VALUE;
-  if (workspace_bytes < kda::pages_compact_bytes(num_pages)) return KDA_ERROR_WORKSPACE_TOO_SMALL;
+  const int64_t need = (int64_t)kda::pages_compact_bytes(num_pages);
+  if (workspace_bytes < (size_t)need) return KDA_ERROR_WORKSPACE_TOO_SMALL;
+  if (overlap(workspace, need, page_refs, re) || overlap(workspace, need, block_table, te) ||
+      overlap(workspace, need, out_refs, re) || overlap(workspace, need, out_table, oe) ||
+      overlap(workspace, need, moved, 4))
+    return KDA_ERROR_INVALID_VALUE;
   a.page_refs = page_refs, a.block_table = block_table;
   a.table_stride = table_stride, a.out_table_stride = out_table_stride;
   a.num_seqs = num_seqs, a.num_pages = num_pages, a.max_pages = max_pages;

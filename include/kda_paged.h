@@ -21,6 +21,8 @@
  * rows table_stride elements apart: entry j of row n holds the tokens j * page_size ..
  * (j + 1) * page_size - 1 of sequence n. seq_lens is int32 [num_seqs], each sequence's length.
  * page_refs is int32 [num_pages]: the number of table entries that hold the page; 0 is free.
+ * Limits: num_pages <= 2^30, num_seqs <= 2^20, heads <= 4096, total_tokens <= 2^30 (attention:
+ * total_tokens * num_q_heads <= 2^30, and keys from 2^31 - 65536 on are not seen).
  *
  * New tokens: sequence n's new tokens are rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 of
  * q, k, v, o (cu_seqlens NULL: total_tokens / num_seqs rows each, which must divide), and are
@@ -54,8 +56,8 @@ extern "C" {
  *               apart; either may be NULL with its output (then its head count is ignored)
  *   positions : int32 [num_tokens], any value
  *   inv_freq  : fp64 [rot_dim / 2], radians per position
- *   q_out, k_out : q or k itself (in place, with its stride), or contiguous and not overlapping q, k
- *               or each other
+ *   q_out, k_out : q or k itself (in place, with its stride; then q and k may lie between each
+ *               other but not overlap), or contiguous and not overlapping q, k or each other
  * head_dim: a multiple of 16 up to 512; rot_dim: a multiple of 16, 16 <= rot_dim <= head_dim.
  */
 enum { KDA_ROPE_INTERLEAVED = 1u, KDA_ROPE_INVERSE = 2u };
@@ -69,7 +71,7 @@ kda_status kda_rope(const void* q, const void* k, const int32_t* positions, cons
  * is stored) and q by their positions on the way: one launch between a layer's projections and
  * its attention. A token whose position is negative or lies in no page is not stored.
  *   q, q_out : as in kda_rope, or both NULL; q_out holds the turned q (with inv_freq NULL q must be
- *              NULL). Either q itself or contiguous.
+ *              NULL). Either q itself (whose rows then do not overlap those of k and v) or contiguous.
  *   k, v     : [rows][num_kv_heads][head_dim]
  * head_dim: a multiple of 16 up to 512. rope_flags: KDA_ROPE_INTERLEAVED or 0.
  */

@@ -316,3 +316,55 @@ def test_binding_refusals_on_the_cpu():
         kda.pages_copy([cache] * 9, one, one)
     with pytest.raises(TypeError):
         kda.pages_free(refs, table, lens, one.long(), 16)
+
+
+# Rows of 4 + 2 heads of 64 bf16: q takes 512 bytes, k 256.
+@pytest.mark.parametrize("kw", [
+    dict(q=A, k=A + 256, qs=384, ks=384, qo=A, ko=6 * A),          # k begins inside q's heads
+    dict(q=A + 128, k=A, qs=384, ks=384, qo=5 * A, ko=A),          # q begins inside k's
+    dict(q=A, k=A + 512, qs=384, ks=512, qo=A, ko=6 * A),          # other strides: rows cross
+])
+def test_rope_in_place_over_the_other_input(kw):
+    assert _rope(**kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=A, k=A + 256, qs=512, ks=512, qo=A),                    # k begins inside q's heads
+    dict(q=A, v=A + 896, qs=512, vs=512, qo=A),                    # v ends inside the next token's q
+])
+def test_append_in_place_over_the_other_inputs(kw):
+    assert _append(**kw) == INVALID
+
+
+@pytest.mark.parametrize("at", ["q", "o", "lse", "kp", "vp"])
+def test_attn_workspace_apart(at):
+    base = dict(q=A, o=2 * A, lse=3 * A, kp=16 * A, vp=32 * A)
+    assert _attn(ws=base[at]) == INVALID
+
+
+def _plan_call(name, **kw):
+    a = dict(refs=A, table=2 * A, ts=8, lens=3 * A, x=4 * A, y=5 * A, count=4, N=4, P=64, M=8, ps=16, granted=6 * A,
+             ws=7 * A, wsb=BIG)
+    a.update(kw)
+    L = _paged._api()
+    rest = (a["count"], a["N"], a["P"], a["M"], a["ps"], a["granted"], a["ws"], a["wsb"], None)
+    if name == "alloc":
+        return L.kda_pages_alloc(a["refs"], a["table"], a["ts"], a["lens"], a["x"], a["y"], *rest)
+    return L.kda_pages_fork(None, 0, a["refs"], a["table"], a["ts"], a["lens"], a["x"], a["y"], *rest)
+
+
+@pytest.mark.parametrize("name", ["alloc", "fork"])
+@pytest.mark.parametrize("kw", [dict(ws=A), dict(ws=2 * A), dict(ws=3 * A), dict(ws=6 * A), dict(granted=A + 4),
+                                dict(granted=2 * A + 64), dict(granted=3 * A), dict(P=(1 << 30) + 1)])
+def test_plan_outputs_apart(name, kw):
+    assert _plan_call(name, **kw) == INVALID
+
+
+def test_page_count_limit():
+    L = _paged._api()
+    assert L.kda_pages_plan_workspace_size(1, 1, (1 << 30) + 1) == 0
+    assert L.kda_pages_compact_workspace_size((1 << 30) + 1) == 0
+    assert L.kda_pages_plan_workspace_size(1, 1, 1 << 30) >= 4 << 30
+    assert _attn(P=(1 << 30) + 1) == INVALID
+    assert _append(P=(1 << 30) + 1) == INVALID
+    assert L.kda_pages_compact(None, 0, A, 2 * A, 8, 4, 64, 8, 3 * A, 4 * A, 8, 5 * A, A, BIG, None) == INVALID
