@@ -336,6 +336,46 @@ def test_same_bits_every_run(new, ctx, D, dtype):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257])
+def test_rows_at_the_borders(rows, dtype):
+    """As many rows as either kernel takes at most, one less and one more, and so at the tiles' sizes."""
+    s = make([rows] * 2, [100, 0], 1, 1, 64, 16, dtype, seed=rows)
+    d = dev(s)
+    check(s, *run(d, cu=False))
+    check(s, *run(d))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_shares_of_many_steps(dtype):
+    """Tiles whose workgroups walk over more steps than one reading of the page table covers (64)."""
+    s = make([300], [40000], 16, 16, 64, 64, dtype, seed=21)
+    o, lse = run(dev(s))
+    some = slice(0, 16, 15)  # (the first and the last head: the rest would take the fp64 form a minute)
+    check(dict(s, q=s["q"][:, some], kc=s["kc"][:, some], vc=s["vc"][:, some]), o[:, some], lse[:, some])
+
+
+def test_two_calls_at_once():
+    """Two batches on two streams, with a workspace each: neither sees the other."""
+    batches = [make([200, 1, 40], [900, 2000, 77], 8, 2, 128, 16, BF16, seed=31),
+               make([1, 1, 1], [3000, 20, 500], 8, 2, 128, 16, BF16, seed=32)]
+    devs = [dev(s) for s in batches]
+    want = [run(d) for d in devs]
+    size = [kda.attn_workspace_size(3, d["q"].shape[0], 8, 2, 128, BF16) for d in devs]
+    work = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in size]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(run(devs[i], workspace=work[i]))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for o, lse in g:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
 def test_other_stream():
     s = make([1, 60, 1, 3], [900, 30, 2000, 77], 8, 2, 128, 16, BF16, seed=13)
     d = dev(s)
