@@ -102,11 +102,16 @@ __device__ __forceinline__ void unit(const T* src, T* dst, int c, int rot, const
   }
 }
 
+// This workgroup's token: a grid holds 2^32 threads in one dimension, so many tokens take two.
+constexpr int kGridTokens = 1 << 22;
+__device__ __forceinline__ int64_t token() { return (int64_t)blockIdx.y * kGridTokens + blockIdx.x; }
+
 // One token per workgroup.
 template <typename T, bool INTER, bool STREAM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   __shared__ f32x2 cs[kMaxDim / 2];
-  const int64_t t = blockIdx.x;
+  const int64_t t = token();
+  if (t >= a.b.total_tokens) return;
   const int half = a.rot_dim / 2;
   for (int j = threadIdx.x; j < half; j += kThreads) cs[j] = turn(a.positions[t], a.inv_freq[j], a.scale, a.inverse);
   __syncthreads();
@@ -135,7 +140,8 @@ template <typename T, bool INTER, bool STREAM>
 __global__ __launch_bounds__(kThreads) void append_kernel(RopeArgs a) {
   __shared__ f32x2 cs[kMaxDim / 2];
   __shared__ int seq, pos, page;
-  const int64_t t = blockIdx.x;
+  const int64_t t = token();
+  if (t >= a.b.total_tokens) return;
   if (threadIdx.x == 0) seq = a.b.cu_seqlens ? 0 : (int)(t / (a.b.total_tokens / a.b.num_seqs));
   __syncthreads();
   if (a.b.cu_seqlens) {
@@ -192,7 +198,9 @@ constexpr int64_t kStreamBytes = 32 << 20;
 
 template <typename T, bool INTER>
 void rope_launch(const RopeArgs& a, bool append) {
-  const dim3 grid((unsigned)a.b.total_tokens);
+  const int64_t tokens = a.b.total_tokens;
+  const dim3 grid((unsigned)(tokens < kGridTokens ? tokens : kGridTokens),
+                  (unsigned)((tokens + kGridTokens - 1) / kGridTokens));
   const int64_t heads = a.num_q_heads + (append ? 2 : 1) * a.num_k_heads;
   const bool stream = a.b.total_tokens * heads * a.head_dim * (int64_t)sizeof(T) > kStreamBytes;
   if (append) {

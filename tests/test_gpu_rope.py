@@ -158,3 +158,22 @@ def test_graph_replay():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), rep
+
+
+def test_more_tokens_than_one_grid_dimension():
+    """2^24 tokens and a few: 2^32 threads and more. Equal bit for bit to calls on parts."""
+    T, D = (1 << 24) + 5, 16
+    f, _ = kda.rope_freqs(D, device=DEV)
+    k = torch.randn((T, 1, D), device=DEV).bfloat16()
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    got = kda.rope(None, k, pos, f)[1]
+    for a, b in ((0, 9), ((1 << 22) - 3, (1 << 22) + 3), (T - 9, T)):
+        assert torch.equal(got[a:b], kda.rope(None, k[a:b], pos[a:b].contiguous(), f)[1])
+    ps = 256
+    P = -(-T // ps)
+    cache = torch.zeros((2, P, 1, ps, D), dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(P, dtype=torch.int32, device=DEV).view(1, P)
+    kda.cache_append(k, k, cache[0], cache[1], table, torch.tensor([T], dtype=torch.int32, device=DEV), inv_freq=f)
+    assert torch.equal(cache[0].view(-1, 1, D)[:T], got)
+    assert torch.equal(cache[1].view(-1, 1, D)[:T], k)
+    assert not cache.view(2, -1)[:, T * D:].any()
