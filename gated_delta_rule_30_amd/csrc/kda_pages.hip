@@ -11,7 +11,7 @@
 // other, so those that do not are issued first, and claims are settled in LDS where they fit. The copies
 // are bound by HBM and run over every (page, plane, 8 KB part).
 // Measured: compaction of 8192 pages (516 MB moved) 96 us, of which 5 each go to the counts and the
-// ranks; a fork of one sequence into four 6.4 us of plan and 3 of rows and copies each.
+// ranks; a fork of one sequence into four 6.4 us of plan and 4 of rows and copies.
 #include "kda_device.h"
 #include "kda_paged_int.h"
 
@@ -234,14 +234,21 @@ __global__ __launch_bounds__(kPlan) void plan_kernel(PagesArgs a) {
   }
 }
 
-// The rows of granted pairs: the child's full pages are the parent's, each counted once more.
-__global__ __launch_bounds__(kCopy) void fork_rows_kernel(PagesArgs a) {
+// What follows the plan of a fork, in one launch (a second one costs the host 3 us). The first count * ny workgroups
+// fill the rows of granted pairs: the child's full pages are the parent's, each counted once more. The others copy the
+// pages that are not full.
+__global__ __launch_bounds__(kCopy) void fork_kernel(PagesArgs a, int ny) {
   const Plan pl = plan_at(a.workspace, a.count, a.num_seqs);
-  const int i = blockIdx.x, full = pl.len[i] / a.page_size;
+  const int groups = a.count * ny;
+  if ((int)blockIdx.x >= groups) {
+    copy_pages(a.pools, pl.from, pl.to, a.count, blockIdx.x - groups, gridDim.x - groups);
+    return;
+  }
+  const int i = blockIdx.x / ny, y = blockIdx.x % ny, full = pl.len[i] / a.page_size;
   if (pl.len[i] < 0) return;
   const int32_t* from = a.block_table + a.parents[i] * a.table_stride;
   int32_t* to = a.block_table + a.seqs[i] * a.table_stride;
-  for (int j = blockIdx.y * kCopy + threadIdx.x; j < full; j += gridDim.y * kCopy) {
+  for (int j = y * kCopy + threadIdx.x; j < full; j += ny * kCopy) {
     const int p = from[j];
     to[j] = p;
     if ((unsigned)p < (unsigned)a.num_pages) atomicAdd(&a.page_refs[p], 1);
@@ -389,12 +396,10 @@ hipError_t launch_pages_alloc(const PagesArgs& a) {
 
 hipError_t launch_pages_fork(const PagesArgs& a) {
   plan_kernel<true><<<1, kPlan, 0, a.stream>>>(a);
-  const unsigned ny = (unsigned)((a.max_pages + 4 * kCopy - 1) / (4 * kCopy));
-  fork_rows_kernel<<<dim3(a.count, ny < 64 ? ny : 64), kCopy, 0, a.stream>>>(a);
-  if (a.pools.n > 0) {
-    const Plan pl = plan_at(a.workspace, a.count, a.num_seqs);
-    copy_kernel<<<copy_grid(a.pools, a.count), kCopy, 0, a.stream>>>(a.pools, pl.from, pl.to, a.count);
-  }
+  // (count is 2^20 at most, and a grid holds 2^32 threads)
+  const int per = (a.max_pages - 1) / (4 * kCopy) + 1, room = (1 << 22) / a.count, ny = per < room ? (per < 64 ? per : 64) : room;
+  const unsigned copies = a.pools.n > 0 ? copy_grid(a.pools, a.count) : 0;
+  fork_kernel<<<(unsigned)(a.count * ny) + copies, kCopy, 0, a.stream>>>(a, ny);
   return hipGetLastError();
 }
 
