@@ -13,14 +13,13 @@
 //    step of a wave is 512 clocks of products and about 400 of vector work; left to themselves the waves
 //    drift into the same phase (the case below, when this was built: 1.69 ms without turns, 1.34 with).
 //  - Loads are made two steps ahead: a step takes 1.1 us, about as long as
-//    a key is on its way from HBM (one step ahead 1370 us, two 1285 to 1257).
+//    a key is on its way from HBM (on one card one step ahead 1370 us, two 1285).
 //  - The output is rescaled only when a maximum grows by more than 2^8: weights up to 2^8 cost
 //    neither the fp32 sums nor the bf16 weights any relative accuracy.
 //  - The tiles' keys are laid end to end and cut into equal shares, one per workgroup; a tile
 //    that is cut leaves partial (o, m, l), joined with those of the row kernel.
-// Measured: 4096 new tokens behind 16384, 32 query heads over 8, D = 128, bf16: 1257 us, 984 TFLOP/s
-// (a library product of 16384^3 bf16 reaches 1381 on the same card; the kernel with its loads of keys and
-// values taken out 1310, so what is left is mostly memory latency and a clock held down by power). fp32: 3
+// Measured: 4096 new tokens behind 16384, 32 query heads over 8, D = 128, bf16: 1257 to 1310 us by
+// card, 945 to 984 TFLOP/s (a library product of 16384^3 bf16 reaches 1381; the clock is held down by power in both). fp32: 3
 // sequences, 432 new tokens over 5392, 16 heads: 106 us; 9.7 GFLOP with the rows that pad the last tiles, at 92 of
 // the 154 TFLOP/s of a library product.
 #include "kda_attn.h"
