@@ -6,9 +6,10 @@
 // Every element is read once and written once, so the kernels are bound by HBM. The angles are
 // shared by all heads of a token: a workgroup forms the sines and cosines of its tokens once, in
 // fp64 turns reduced to [-1/2, 1/2] (an fp32 product p f would be off by up to 2^-24 p f radians,
-// 0.06 at p f = 10^6), keeps them in LDS as fp32, and then streams the heads: one unit is 16 channels
-// (8 pairs) of one head, two 16-byte loads and stores in bf16.
-// Measured: 16384 tokens of 32 + 8 heads of 128, bf16: 336 MB in 54 us, 6.2 TB/s. The append of 20 chunks of 64 to
+// 0.06 at p f = 10^6), keeps them in LDS as fp32, and then streams the heads: one unit is two
+// 16-byte loads and stores of one head.
+// Measured: 16384 tokens of 32 + 8 heads of 128, bf16, either pairing: 336 MB in 49 to 54 us, 6.2 to 6.9 TB/s (fp32, 8192
+// tokens: 50 us; with 16 channels in a row per lane fp32 took 65, heads of 256 up to 113 where they take 39). The append of 20 chunks of 64 to
 // 2048 tokens (213 MB): 34 to 35 us, 6.2 TB/s; of 256 single tokens (6 MB): 4.5 us, launch and latency.
 #include "kda_device.h"
 #include "kda_paged_int.h"
@@ -20,19 +21,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxDim = 512;
 
-// 8 consecutive channels as fp32, and back with one rounding each.
-__device__ __forceinline__ void load8(const bf16* p, float (&x)[8]) {
+// Channels of 16 bytes, as fp32, and back with one rounding each.
+template <typename T>
+constexpr int kWide = 16 / (int)sizeof(T);
+__device__ __forceinline__ void load(const bf16* p, float (&x)[8]) {
   const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+__device__ __forceinline__ void load(const float* p, float (&x)[4]) {
+  const f32x4 v = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
+  for (int i = 0; i < 4; ++i) x[i] = v[i];
 }
 template <bool STREAM>
-__device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
+__device__ __forceinline__ void store(bf16* p, const float (&x)[8]) {
   bf16x8 v;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = (bf16)x[i];
@@ -40,15 +43,10 @@ __device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
   else *reinterpret_cast<bf16x8*>(p) = v;
 }
 template <bool STREAM>
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  const f32x4 a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
-  f32x4* d = reinterpret_cast<f32x4*>(p);
-  if constexpr (STREAM) {
-    __builtin_nontemporal_store(a, d);
-    __builtin_nontemporal_store(b, d + 1);
-  } else {
-    d[0] = a, d[1] = b;
-  }
+__device__ __forceinline__ void store(float* p, const float (&x)[4]) {
+  const f32x4 v = {x[0], x[1], x[2], x[3]};
+  if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(p));
+  else *reinterpret_cast<f32x4*>(p) = v;
 }
 
 // Sine and cosine of p * f (radians) times scale. The angle is formed in turns, f / (2 pi) and its
@@ -63,20 +61,21 @@ __device__ __forceinline__ f32x2 turn(int p, double f, float scale, bool inverse
   return f32x2{scale * c, inverse ? -scale * s : scale * s};
 }
 
-// One unit: channels of one head at src to dst (either may be the other). c: the unit's index
-// in the head; units below rot / 16 turn 8 pairs, the others copy 16 channels.
+// One unit: twice 16 bytes of one head at src to dst (either may be the other), half of the turned channels (or of the
+// others) apart, so that what the lanes of a wave load or store at once lies side by side. c: the unit's index in the
+// head, the turning ones first.
 template <typename T, bool INTER, bool STREAM>
-__device__ __forceinline__ void unit(const T* src, T* dst, int c, int rot, const f32x2* cs) {
-  float x[8], y[8];
-  if (16 * c < rot) {
-    const int a = INTER ? 16 * c : 8 * c, b = INTER ? 16 * c + 8 : rot / 2 + 8 * c;
-    load8(src + a, x);
-    load8(src + b, y);
-    const f32x2* t = cs + 8 * c;
+__device__ __forceinline__ void unit(const T* src, T* dst, int c, int dim, int rot, const f32x2* cs) {
+  constexpr int W = kWide<T>;
+  float x[W], y[W];
+  if (2 * W * c < rot) {
+    const int a = W * c, b = rot / 2 + W * c;
+    load(src + a, x);
+    load(src + b, y);
     if constexpr (INTER) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x2 u = t[i], w = t[4 + i];
+      for (int i = 0; i < W / 2; ++i) {
+        const f32x2 u = cs[a / 2 + i], w = cs[b / 2 + i];
         const float x1 = x[2 * i], x2 = x[2 * i + 1], y1 = y[2 * i], y2 = y[2 * i + 1];
         x[2 * i] = x1 * u[0] - x2 * u[1];
         x[2 * i + 1] = x2 * u[0] + x1 * u[1];
@@ -85,20 +84,21 @@ __device__ __forceinline__ void unit(const T* src, T* dst, int c, int rot, const
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const f32x2 u = t[i];
+      for (int i = 0; i < W; ++i) {
+        const f32x2 u = cs[a + i];
         const float x1 = x[i], x2 = y[i];
         x[i] = x1 * u[0] - x2 * u[1];
         y[i] = x2 * u[0] + x1 * u[1];
       }
     }
-    store8<STREAM>(dst + a, x);
-    store8<STREAM>(dst + b, y);
+    store<STREAM>(dst + a, x);
+    store<STREAM>(dst + b, y);
   } else if (dst != src) {
-    load8(src + 16 * c, x);
-    load8(src + 16 * c + 8, y);
-    store8<STREAM>(dst + 16 * c, x);
-    store8<STREAM>(dst + 16 * c + 8, y);
+    const int a = rot / 2 + W * c, b = a + (dim - rot) / 2;
+    load(src + a, x);
+    load(src + b, y);
+    store<STREAM>(dst + a, x);
+    store<STREAM>(dst + b, y);
   }
 }
 
@@ -115,14 +115,14 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
   const int half = a.rot_dim / 2;
   for (int j = threadIdx.x; j < half; j += kThreads) cs[j] = turn(a.positions[t], a.inv_freq[j], a.scale, a.inverse);
   __syncthreads();
-  const int C = a.head_dim / 16, heads = a.num_q_heads + a.num_k_heads;
+  const int C = a.head_dim / (2 * kWide<T>), heads = a.num_q_heads + a.num_k_heads;
   for (int u = threadIdx.x; u < heads * C; u += kThreads) {
     const int h = u / C, c = u - h * C;
     const bool isq = h < a.num_q_heads;
     const int hh = isq ? h : h - a.num_q_heads;
     const T* src = (const T*)(isq ? a.q : a.k) + t * (isq ? a.q_stride : a.k_stride) + hh * a.head_dim;
     T* dst = (T*)(isq ? a.q_out : a.k_out) + t * (isq ? a.q_out_stride : a.k_out_stride) + hh * a.head_dim;
-    unit<T, INTER, STREAM>(src, dst, c, a.rot_dim, cs);
+    unit<T, INTER, STREAM>(src, dst, c, a.head_dim, a.rot_dim, cs);
   }
 }
 
@@ -171,13 +171,13 @@ __global__ __launch_bounds__(kThreads) void append_kernel(RopeArgs a) {
     for (int j = threadIdx.x; j < a.rot_dim / 2; j += kThreads) cs[j] = turn(pos, a.inv_freq[j], a.scale, false);
     __syncthreads();
   }
-  const int D = a.head_dim, C = D / 16, ps = a.b.page_size;
+  const int D = a.head_dim, C = D / (2 * kWide<T>), ps = a.b.page_size;
   const int rot = a.inv_freq ? a.rot_dim : 0;
   const int nq = a.q ? a.num_q_heads : 0, nk = a.num_k_heads, heads = nq + 2 * nk;
   for (int u = threadIdx.x; u < heads * C; u += kThreads) {
     const int h = u / C, c = u - h * C;
     if (h < nq) {
-      unit<T, INTER, STREAM>((const T*)a.q + t * a.q_stride + h * D, (T*)a.q_out + t * a.q_out_stride + h * D, c, rot, cs);
+      unit<T, INTER, STREAM>((const T*)a.q + t * a.q_stride + h * D, (T*)a.q_out + t * a.q_out_stride + h * D, c, D, rot, cs);
       continue;
     }
     if (page < 0) continue;
@@ -185,10 +185,11 @@ __global__ __launch_bounds__(kThreads) void append_kernel(RopeArgs a) {
     const int hh = isk ? h - nq : h - nq - nk;
     const int64_t at = ((int64_t)hh * ps + pos % ps) * D;
     if (isk)
-      unit<T, INTER, STREAM>((const T*)a.k + t * a.k_stride + hh * D, (T*)a.k_pages + page * a.k_page_stride + at, c, rot,
-                             cs);
+      unit<T, INTER, STREAM>((const T*)a.k + t * a.k_stride + hh * D, (T*)a.k_pages + page * a.k_page_stride + at, c, D,
+                             rot, cs);
     else
-      unit<T, INTER, STREAM>((const T*)a.v + t * a.v_stride + hh * D, (T*)a.v_pages + page * a.v_page_stride + at, c, 0, cs);
+      unit<T, INTER, STREAM>((const T*)a.v + t * a.v_stride + hh * D, (T*)a.v_pages + page * a.v_page_stride + at, c, D, 0,
+                             cs);
   }
 }
 
